@@ -117,6 +117,20 @@ cudaError_t launch_assign_tc(DType dt, const void *X, const void *C, const float
                              int D, int K, int Kpad, const float *xnorm, int32_t *labels, float *mindist,
                              NearTies ties, DevCtl ctl, int num_sms, cudaStream_t s);
 
+// ---- label_sort.cu: stable sort of points by label -------------------------
+// The B*N points in label order: skeys[j] = b*K + label of the j-th, perm[j]
+// its row b*N + i; points of one label in ascending row order.  drop: labels
+// outside [0, K) are left out -- they get the key B*K and lie behind the rest
+// (behind their problem's rest when B > 1) -- and -1 is not an error; without
+// drop they count as 0.
+struct LabelSort {
+  const int32_t *skeys, *perm;
+};
+size_t label_sort_bytes(int64_t Ntot, int64_t Ktot, int B, bool drop);
+// ws of label_sort_bytes(B * N, B * K, B, drop), where the result lies; B * N > 0.
+cudaError_t launch_label_sort(const int32_t *labels, int B, int N, int K, bool drop, void *ws, int *status,
+                              cudaStream_t s, LabelSort *out);
+
 // ---- update.cu: sort-inverse update ---------------------------------------
 enum UpdateMode : int { kMean = 0, kAccumulate = 1 };
 struct UpdateArgs {

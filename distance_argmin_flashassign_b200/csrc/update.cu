@@ -4,12 +4,8 @@
 // scatter of the update stage by an explicitly built inverse mapping and
 // segment-level localized reductions.  Here:
 //
-//   1. stable LSD radix sort of the cluster ids (11-bit digits, one pass for
-//      up to 2,048 clusters, two for up to 2^22; a batch of problems whose N
-//      is whole 4096-key tiles takes one pass on the label per problem):
-//      per-tile digit histograms, a per-digit scan over tiles, and a scatter
-//      whose within-tile ranks come from shared-memory digit masks -- the
-//      sorted point ids are the inverse map (cluster -> its points);
+//   1. stable radix sort of the cluster ids (label_sort.cu): the sorted point
+//      ids are the inverse map (cluster -> its points);
 //   2. segmented sums: the sorted order is cut into equal chunks of R
 //      positions, one worker per chunk (a half warp for 256-byte rows), so a
 //      hot cluster (Zipf skew) is spread over many workers instead of
@@ -25,79 +21,10 @@
 //
 // Batched problems are one problem over B*K clusters: point (b, i) gets key
 // b*K + label.
+#include "chain.cuh"
 #include "fk_internal.h"
 
 namespace fk {
-
-// Kernels of the update are launched with programmatic stream serialization:
-// a kernel may start (set up shared memory, compute addresses) while the one
-// before it drains, and waits here before its first read of that kernel's
-// results.  The wait returns once the previous grid has completed and its
-// writes are visible.
-__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                  Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-constexpr int kSortThreads = 256;
-constexpr int kSortItems = 16;
-constexpr int kSortTile = kSortThreads * kSortItems;  // 4096 keys per tile
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxDigitBits = 11;
-constexpr int kMaxBins = 1 << kMaxDigitBits;
-
-struct SortPlan {
-  int npass;
-  int shift[2], bits[2];
-  int T;          // tiles
-  int seg_tiles;  // > 0: one pass on the label digit, problems of seg_tiles whole tiles each
-};
-
-static int ceil_log2(long long v) {
-  int b = 0;
-  while ((1ll << b) < v) ++b;
-  return b;
-}
-
-// A batch of B problems whose N is a whole number of tiles is sorted in one
-// pass on the label alone when the key b*K + label would need two: the
-// problems' points are already in problem order, and each tile belongs to
-// one problem, so ranking a tile's points by label and placing problem b's
-// runs at b*N gives the order of a stable sort by key.
-static SortPlan plan_sort(long long Ntot, long long Ktot, int B) {
-  SortPlan p{};
-  int bits = ceil_log2(Ktot);
-  if (bits < 1) bits = 1;
-  p.npass = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
-  const int w = (bits + p.npass - 1) / p.npass;
-  int sh = 0;
-  for (int i = 0; i < p.npass; ++i) {
-    p.shift[i] = sh;
-    p.bits[i] = (bits - sh) < w ? (bits - sh) : w;
-    sh += p.bits[i];
-  }
-  p.T = (int)((Ntot + kSortTile - 1) / kSortTile);
-  if (B > 1 && p.npass > 1 && (Ntot / B) % kSortTile == 0 && ceil_log2(Ktot / B) <= kMaxDigitBits) {
-    p.npass = 1;
-    p.shift[0] = 0;
-    p.bits[0] = ceil_log2(Ktot / B) < 1 ? 1 : ceil_log2(Ktot / B);
-    p.seg_tiles = (int)(Ntot / B / kSortTile);
-  }
-  return p;
-}
 
 // Positions per segment-sum worker: enough workers for about one wave of a
 // B200 (148 SMs x 48 resident half-warp workers), at least 128; two full
@@ -111,274 +38,6 @@ static int chunk_rows_R(long long Ntot) {
   if (R > 512) R = (Ntot + 2 * kWave - 1) / (2 * kWave);
   R = (R + 31) / 32 * 32;
   return (int)(R < 128 ? 128 : R);
-}
-
-// --------------------------------------------------------------- sorting --
-// Sort key of position pos from its label: b*K + label for problem b.  A
-// label outside [0, K) counts as 0 and sets `bad`; the caller records it
-// once, after all of its loads, so that no atomic sits between them.
-__device__ __forceinline__ int key_of_label(int lab, int pos, int N, int K, int B, bool &bad) {
-  if ((unsigned)lab >= (unsigned)K) {
-    bad = true;
-    lab = 0;
-  }
-  return B > 1 ? (pos / N) * K + lab : lab;
-}
-
-// SEG: one pass per problem (the digit is the label), see plan_sort.
-template <bool FIRST, bool SEG>
-__global__ void __launch_bounds__(kSortThreads) radix_hist_kernel(const int32_t *__restrict__ keys, int Ntot,
-                                                                  int N, int K, int B, int shift, int nbins,
-                                                                  int T, int *__restrict__ H,
-                                                                  int *status, int seg_tiles) {
-  __shared__ int hist[kMaxBins + 1];
-  for (int i = threadIdx.x; i <= nbins; i += kSortThreads) hist[i] = 0;
-  __syncthreads();
-  wait_prior_grid();
-  const int base = blockIdx.x * kSortTile;
-  // all of the thread's keys are loaded before any is counted (16 loads in
-  // flight), then counted with shared-memory atomics
-  int v[kSortItems];
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it) {
-    const int pos = base + it * kSortThreads + threadIdx.x;
-    v[it] = pos < Ntot ? keys[pos] : 0;
-  }
-  bool bad = false;
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it) {
-    const int pos = base + it * kSortThreads + threadIdx.x;
-    int d = nbins;  // spare bin for positions past the end
-    if (pos < Ntot) {
-      const int key = FIRST ? key_of_label(v[it], pos, N, K, B, bad) : v[it];
-      // one pass per problem: the digit is the label (each tile lies in one problem)
-      d = SEG ? key - ((int)blockIdx.x / seg_tiles) * K : (key >> shift) & (nbins - 1);
-    }
-    atomicAdd(&hist[d], 1);
-  }
-  if (bad) record_status(status, kStBadLabel);
-  __syncthreads();
-  for (int i = threadIdx.x; i < nbins; i += kSortThreads) H[(size_t)i * T + blockIdx.x] = hist[i];
-}
-
-// In place: row d of H becomes the exclusive prefix over tiles; totals[d] = row sum.
-__global__ void __launch_bounds__(256) scan_rows_kernel(int *__restrict__ H, int T, int nbins,
-                                                        int *__restrict__ totals) {
-  const int w = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  wait_prior_grid();
-  if (w >= nbins) return;
-  int *row = H + (size_t)w * T;
-  int carry = 0;
-  // 256 tiles per round: all of a lane's loads are issued before any is
-  // scanned, so a round costs one memory round trip
-  constexpr int kPerLane = 8;
-  for (int t0 = 0; t0 < T; t0 += 32 * kPerLane) {
-    int v[kPerLane];
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      const int tt = t0 + 32 * i + lane;
-      v[i] = tt < T ? row[tt] : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-      int incl = v[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += n;
-      }
-      const int tt = t0 + 32 * i + lane;
-      if (tt < T) row[tt] = carry + incl - v[i];
-      carry += __shfl_sync(0xffffffffu, incl, 31);
-    }
-  }
-  if (lane == 0) totals[w] = carry;
-}
-
-// ints of the region that holds the warps' digit masks while keys are
-// ranked, then the tile's keys and values in sorted order
-static __host__ __device__ int scatter_xbuf_ints(int nbins) {
-  return 2 * kSortTile > kSortWarps * nbins ? 2 * kSortTile : kSortWarps * nbins;
-}
-static size_t scatter_smem_bytes(int nbins) {
-  return (size_t)(2 * nbins + kSortWarps + scatter_xbuf_ints(nbins)) * 4 + (size_t)kSortWarps * (nbins + 1) * 4;
-}
-
-template <bool FIRST, bool SEG>
-__global__ void __launch_bounds__(kSortThreads) radix_scatter_kernel(
-    const int32_t *__restrict__ keys_in, const int32_t *__restrict__ vals_in, int32_t *__restrict__ keys_out,
-    int32_t *__restrict__ vals_out, int Ntot, int N, int K, int B, int shift, int nbins, int T,
-    const int *__restrict__ H, const int *__restrict__ totals, int *status, int seg_tiles) {
-  extern __shared__ int sh[];
-  const int stride = nbins + 1;
-  int *dbase = sh;                                                   // [nbins]
-  int *tstart = sh + nbins;                                          // [nbins]
-  int *wsum = sh + 2 * nbins;                                        // [kSortWarps]
-  int *keys_s = sh + 2 * nbins + kSortWarps;                         // [kSortTile]
-  int *vals_s = keys_s + kSortTile;                                  // [kSortTile]
-  unsigned *wmask = reinterpret_cast<unsigned *>(keys_s);            // [kSortWarps][nbins], same place
-  int *wcnt = keys_s + scatter_xbuf_ints(nbins);                     // [kSortWarps][nbins + 1]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // one pass per problem (SEG): this tile's problem; the digit is the label
-  // and the problem's runs start at pb * N
-  const int pb = SEG ? (int)blockIdx.x / seg_tiles : 0;
-  auto digit = [&](int key) { return SEG ? key - pb * K : (key >> shift) & (nbins - 1); };
-  wait_prior_grid();
-  // the warp's 512 consecutive keys and values are loaded first, so that
-  // their latency overlaps the digit-base reads below
-  int keyr[kSortItems], valr[kSortItems], locr[kSortItems];
-  const int base = blockIdx.x * kSortTile + warp * (kSortItems * 32);
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it) {
-    const int pos = base + it * 32 + lane;
-    keyr[it] = pos < Ntot ? keys_in[pos] : 0;
-    valr[it] = pos < Ntot ? (FIRST ? pos : vals_in[pos]) : 0;
-  }
-
-  // digit base of this tile = exclusive scan of digit totals + tile prefix;
-  // both reads of a thread's digits are issued before either is used
-  constexpr int kPer = kMaxBins / kSortThreads;  // digits per thread, at most
-  const int per = (nbins + kSortThreads - 1) / kSortThreads;
-  int tv[kPer], hv[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int d = tid * per + i;
-    const bool ok = i < per && d < nbins;
-    if (SEG) {
-      // the problem's count of digit d and the count in its tiles before
-      // this one, from the prefix over all tiles at the problem's bounds
-      const int t0 = pb * seg_tiles, t1 = t0 + seg_tiles;
-      const int p0 = ok ? H[(size_t)d * T + t0] : 0;
-      const int p1 = ok ? (t1 < T ? H[(size_t)d * T + t1] : totals[d]) : 0;
-      tv[i] = p1 - p0;
-      hv[i] = (ok ? H[(size_t)d * T + blockIdx.x] : 0) - p0;
-    } else {
-      tv[i] = ok ? totals[d] : 0;
-      hv[i] = ok ? H[(size_t)d * T + blockIdx.x] : 0;
-    }
-  }
-  int s = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) s += tv[i];
-  int incl = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  for (int i = tid; i < kSortWarps * stride; i += kSortThreads) wcnt[i] = 0;
-  for (int i = tid; i < kSortWarps * nbins; i += kSortThreads) wmask[i] = 0u;
-  __syncthreads();
-  int run = incl - s + pb * N;
-  for (int w = 0; w < warp; ++w) run += wsum[w];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int d = tid * per + i;
-    if (i < per && d < nbins) dbase[d] = run + hv[i];
-    run += tv[i];
-  }
-
-  // stable ranks within each warp's consecutive keys.  The lanes that hold
-  // the same digit find each other through shared memory: each sets its bit
-  // in the warp's mask word of its digit and reads the word back (on this
-  // GPU much cheaper than a ballot per digit bit or match.any, whose cost
-  // grows with the number of distinct digits).  The lowest of them clears
-  // the word and adds the group's size to the warp's count of that digit;
-  // the count before the add, broadcast after all of the warp's keys are
-  // counted, is where the group starts.
-  const unsigned lt_mask = (1u << lane) - 1u;
-  int *mycnt = wcnt + warp * stride;
-  unsigned *mymask = wmask + warp * nbins;
-  unsigned peer[kSortItems];
-  bool bad = false;
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it) {
-    const int pos = base + it * 32 + lane;
-    const bool valid = pos < Ntot;
-    int d = 0;
-    if (valid) {
-      if (FIRST) keyr[it] = key_of_label(keyr[it], pos, N, K, B, bad);
-      d = digit(keyr[it]);
-    }
-    if (valid) atomicOr(mymask + d, 1u << lane);
-    __syncwarp();
-    const unsigned peers = valid ? mymask[d] : 0u;
-    __syncwarp();
-    int c = 0;
-    if (valid && lane == __ffs(peers) - 1) {
-      mymask[d] = 0u;
-      c = atomicAdd(mycnt + d, __popc(peers));
-    }
-    __syncwarp();  // the next key's mask and add come after these
-    peer[it] = peers;
-    locr[it] = c;
-  }
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it)
-    locr[it] = __shfl_sync(0xffffffffu, locr[it], (__ffs(peer[it]) - 1) & 31) + __popc(peer[it] & lt_mask);
-  if (bad) record_status(status, kStBadLabel);
-  __syncthreads();  // masks done: the region holds keys and values from here on
-  // per digit: exclusive prefix over warps (in place) and the tile's count,
-  // then the exclusive scan of the tile's counts over digits: where each
-  // digit's run starts in the tile's sorted order
-  int cnt[kPer];
-  int tsum = 0;
-  for (int i = 0; i < per; ++i) {
-    const int d = tid * per + i;
-    int r = 0;
-    if (d < nbins)
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int t = wcnt[w * stride + d];
-        wcnt[w * stride + d] = r;
-        r += t;
-      }
-    cnt[i] = r;
-    tsum += r;
-  }
-  int tincl = tsum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, tincl, o);
-    if (lane >= o) tincl += n;
-  }
-  __syncthreads();  // everyone is done reading wsum (digit bases above)
-  if (lane == 31) wsum[warp] = tincl;
-  __syncthreads();
-  int trun = tincl - tsum;
-  for (int w = 0; w < warp; ++w) trun += wsum[w];
-  for (int i = 0; i < per; ++i) {
-    const int d = tid * per + i;
-    if (d < nbins) tstart[d] = trun;
-    trun += cnt[i];
-  }
-  __syncthreads();
-  // exchange through shared memory into the tile's sorted order ...
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it) {
-    const int pos = base + it * 32 + lane;
-    if (pos < Ntot) {
-      const int d = digit(keyr[it]);
-      const int lp = tstart[d] + mycnt[d] + locr[it];
-      keys_s[lp] = keyr[it];
-      vals_s[lp] = valr[it];
-    }
-  }
-  __syncthreads();
-  // ... and write it out in that order: consecutive threads store
-  // consecutive positions of a digit's run
-  const int nvalid = (Ntot - blockIdx.x * kSortTile) < kSortTile ? (Ntot - blockIdx.x * kSortTile) : kSortTile;
-#pragma unroll
-  for (int it = 0; it < kSortItems; ++it) {
-    const int idx = it * kSortThreads + tid;
-    if (idx < nvalid) {
-      const int key = keys_s[idx];
-      const int d = digit(key);
-      const int o = dbase[d] + (idx - tstart[d]);
-      keys_out[o] = key;
-      vals_out[o] = vals_s[idx];
-    }
-  }
 }
 
 // Segment offsets are written by the segment-sum warps: at every position
@@ -956,28 +615,20 @@ __global__ void __launch_bounds__(256) divide_acc_kernel(const double *__restric
 static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct UpdateWs {
-  int32_t *kA, *vA, *kB, *vB;
-  int *H, *totals, *off;
+  void *sort;
+  int *off;
   float *parts;
   size_t bytes;
 };
 
 static UpdateWs carve(void *base, long long Ntot, long long Ktot, int D, int B) {
-  const SortPlan sp = plan_sort(Ntot, Ktot, B);
   const int R = chunk_rows_R(Ntot);
   const long long nchunks = (Ntot + R - 1) / R;
-  int maxbins = 0;
-  for (int i = 0; i < sp.npass; ++i) maxbins = (1 << sp.bits[i]) > maxbins ? (1 << sp.bits[i]) : maxbins;
   UpdateWs w{};
   char *p = (char *)base;
   size_t o = 0;
   auto take = [&](size_t n) { char *r = p ? p + o : nullptr; o += al256(n); return r; };
-  w.kA = (int32_t *)take((size_t)Ntot * 4);
-  w.vA = (int32_t *)take((size_t)Ntot * 4);
-  w.kB = (int32_t *)take((size_t)Ntot * 4);
-  w.vB = (int32_t *)take((size_t)Ntot * 4);
-  w.H = (int *)take((size_t)maxbins * sp.T * 4);
-  w.totals = (int *)take((size_t)maxbins * 4);
+  w.sort = take(label_sort_bytes(Ntot, Ktot, B, false));
   w.off = (int *)take((size_t)(Ktot + 1) * 4);
   w.parts = (float *)take((size_t)nchunks * 2 * D * 4);
   w.bytes = o;
@@ -1060,43 +711,11 @@ cudaError_t launch_update(const UpdateArgs &a, void *ws, size_t ws_bytes, DevCtl
   if (Ntot == 0) return cudaSuccess;
   const UpdateWs w = carve(ws, Ntot, Ktot, a.D, a.B);
   if (w.bytes > ws_bytes) return cudaErrorInvalidValue;
-  const SortPlan sp = plan_sort(Ntot, Ktot, a.B);
   const int N = (int)Ntot;
-  int nl = 0;
-
-  {  // the scatter's tile exchange needs more than the default 48 KB of shared memory
-    static bool configured[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 64 && !configured[dev]) {
-      const int most = (int)scatter_smem_bytes(kMaxBins);
-      cudaFuncSetAttribute(radix_scatter_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-      cudaFuncSetAttribute(radix_scatter_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-      cudaFuncSetAttribute(radix_scatter_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-      configured[dev] = true;
-    }
-  }
-  const int32_t *kin = a.labels, *vin = nullptr;
-  int32_t *kout = w.kA, *vout = w.vA;
-  for (int pass = 0; pass < sp.npass; ++pass) {
-    const int nbins = 1 << sp.bits[pass];
-    const bool seg = sp.seg_tiles > 0;  // one pass, so pass == 0
-    const auto hist = pass > 0 ? radix_hist_kernel<false, false> : seg ? radix_hist_kernel<true, true>
-                                                                          : radix_hist_kernel<true, false>;
-    launch_chained(hist, dim3(sp.T), dim3(kSortThreads), 0, s, kin, N, a.N, a.K, a.B, sp.shift[pass], nbins, sp.T, w.H,
-                   ctl.status, sp.seg_tiles);
-    launch_chained(scan_rows_kernel, dim3((nbins + 7) / 8), dim3(256), 0, s, w.H, sp.T, nbins, w.totals);
-    const auto scatter = pass > 0 ? radix_scatter_kernel<false, false>
-                                  : seg ? radix_scatter_kernel<true, true> : radix_scatter_kernel<true, false>;
-    launch_chained(scatter, dim3(sp.T), dim3(kSortThreads), scatter_smem_bytes(nbins), s, kin, vin, kout, vout, N, a.N,
-                   a.K, a.B, sp.shift[pass], nbins, sp.T, w.H, w.totals, ctl.status, sp.seg_tiles);
-    nl += 3;
-    kin = kout;
-    vin = vout;
-    kout = (kout == w.kA) ? w.kB : w.kA;
-    vout = (vout == w.vA) ? w.vB : w.vA;
-  }
-  const int32_t *skeys = kin, *perm = vin;
+  LabelSort order;
+  cudaError_t e = launch_label_sort(a.labels, a.B, a.N, a.K, false, w.sort, ctl.status, s, &order);
+  if (e != cudaSuccess) return e;
+  const int32_t *skeys = order.skeys, *perm = order.perm;
   const int R = chunk_rows_R(Ntot);
   const int KT = (int)Ktot;
   switch (a.dt) {
@@ -1121,8 +740,7 @@ cudaError_t launch_update(const UpdateArgs &a, void *ws, size_t ws_bytes, DevCtl
   else
     launch_chained(seg_finalize_kernel<kAccumulate>, dim3((int)fgrid), dim3(1024), 0, s, w.off, (int)Ktot, a.D, R, w.parts,
                    nullptr, nullptr, a.acc, a.cnt);
-  nl += 2;
-  count_launches(nl);
+  count_launches(2);
   return cudaGetLastError();
 }
 
