@@ -11,12 +11,15 @@ The functions carry the C names (see ``include/fk.h``) and take torch tensors:
 * ``fk_update(X, labels, C, counts=None)``            (C updated in place)
 * ``fk_lloyd(X, C, iters, labels=None, mindist=None, counts=None)``
 * ``fk_lloyd_ooc(X_host, C_host, iters, chunk_rows, labels_host=None, counts_host=None)``
+* ``fk_lookup(T, ids, scale=1.0)``, ``fk_lookup_grad(dY, ids, K, scale=1.0)``
+* ``fk_balance(Z, ids, mask=None, coef=1.0)``, ``fk_balance_grad(Z, counts, tokens, lse, M, coef=1.0)``
 
 A 3-D ``X`` (B x N x D) selects the batched entry points.  Failures raise
 ``FKError`` carrying the status code and the library's message.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -73,6 +76,12 @@ def _load():
         "fk_debug_inject": [I, I64],
         "fk_gauss_sum": [V, I64, I, I, V, I, V, I, ctypes.c_float, V, V, V],
         "fk_seed_kmeanspp": [V, I64, I, I, I, V, V, V],
+        "fk_lookup": [V, I, I, I, I, V, I64, ctypes.c_float, V, I, V],
+        "fk_lookup_grad_workspace": [I, I64, I, I, I],
+        "fk_lookup_grad": [V, I, I64, I, I, V, I, ctypes.c_float, V, I, I, V, I64, V],
+        "fk_balance_workspace": [I, I64, I, I],
+        "fk_balance": [V, I, I64, I, I, V, I, V, ctypes.c_float, V, V, V, V, V, V, I64, V],
+        "fk_balance_grad": [V, I, I64, I, I, V, V, V, I, ctypes.c_float, V, V, V],
         "fk_version": [],
     }
     for name, args in sig.items():
@@ -83,6 +92,8 @@ def _load():
     lib.fk_last_error_message.restype = ctypes.c_char_p
     lib.fk_launch_count.restype = ctypes.c_uint64
     lib.fk_bias_len.restype = ctypes.c_int64
+    lib.fk_lookup_grad_workspace.restype = ctypes.c_int64
+    lib.fk_balance_workspace.restype = ctypes.c_int64
     return lib
 
 
@@ -93,7 +104,8 @@ ABI_NAMES = ("fk_bias_len", "fk_prepare_centroids", "fk_prepare_points", "fk_ass
              "fk_lloyd_fused", "fk_assign_top2", "fk_lloyd_batched", "fk_lloyd_ooc", "fk_sync", "fk_status_string", "fk_get_last_error",
              "fk_last_error_message", "fk_launch_count", "fk_assign_path", "fk_set_assign_path",
              "fk_set_wait_timeout_ns", "fk_debug_wait_timeout", "fk_release_workspace", "fk_debug_inject",
-             "fk_gauss_sum", "fk_seed_kmeanspp", "fk_version")
+             "fk_gauss_sum", "fk_seed_kmeanspp", "fk_lookup", "fk_lookup_grad_workspace", "fk_lookup_grad",
+             "fk_balance_workspace", "fk_balance", "fk_balance_grad", "fk_version")
 
 
 def _check(status: int) -> None:
@@ -329,6 +341,143 @@ def fk_seed_kmeanspp(X, K, u, centers=None, stream=None):
     _check(lib.fk_seed_kmeanspp(_ptr(X), N, D, _dtype(X), K, ctypes.c_void_p(u.ctypes.data), _ptr(centers),
                                 _stream(stream)))
     return centers
+
+
+# ---------------------------------------------------------- codebook calls --
+# These check every tensor they are given, run on the tensors' device whatever
+# the current one is, and allocate what they return on the stream they run on.
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _book_stream(device, stream):
+    """(the raw stream of a call on ``device``, the context for its allocations and launches)"""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    if stream is None:
+        raw = torch.cuda.current_stream(device).cuda_stream
+        if device.index == torch.cuda.current_device():
+            return raw, contextlib.nullcontext()
+        return raw, torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _book_workspace(workspace, size, device):
+    """The workspace argument of a call that needs ``size`` bytes: the caller's
+    tensor, none (the library's scratch), or under stream capture, where the
+    library has none to give, one of the graph's own pool."""
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+            raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
+        return workspace, workspace.numel()
+    if torch.cuda.is_current_stream_capturing():
+        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device=device)
+        return workspace, workspace.numel()
+    return None, 0
+
+
+def fk_lookup(T, ids, scale=1.0, Y=None, dtype=None, stream=None):
+    """Rows of a codebook by label: Y = scale * T[ids], in ``dtype`` (T's by
+    default); label -1 gives a zero row.  T K x D with ids N, or B x K x D with
+    ids B x N."""
+    B, K, D, bat = _dims(T)
+    N = ids.shape[-1] if ids.dim() else 0
+    lead = (B, N) if bat else (N,)
+    dt = _dtype(T)
+    _need(T, "T", T.dtype, T.shape, T.device)
+    _need(ids, "ids", torch.int32, lead, T.device)
+    raw, ctx = _book_stream(T.device, stream)
+    with ctx:
+        if Y is None:
+            Y = torch.empty(lead + (D,), dtype=dtype or T.dtype, device=T.device)
+        _need(Y, "Y", dtype or Y.dtype, lead + (D,), T.device)
+        _check(lib.fk_lookup(T.data_ptr(), B, K, D, dt, ids.data_ptr(), N, scale, Y.data_ptr(), _dtype(Y), raw))
+    return Y
+
+
+def fk_lookup_grad(dY, ids, K, scale=1.0, dT=None, dtype=None, accumulate=False, workspace=None, stream=None):
+    """Gradient of ``fk_lookup`` with respect to the codebook: dT[k] = scale *
+    the sum of dY's rows with label k (fp32 sums in a fixed order), in ``dtype``
+    (fp32 by default).  ``accumulate`` adds to ``dT`` instead of replacing it.
+    dY N x D with ids N, or B x N x D with ids B x N."""
+    B, N, D, bat = _dims(dY)
+    shape = (B, K, D) if bat else (K, D)
+    dt = _dtype(dY)
+    _need(dY, "dY", dY.dtype, dY.shape, dY.device)
+    _need(ids, "ids", torch.int32, ((B, N) if bat else (N,)), dY.device)
+    if accumulate and dT is None:
+        raise ValueError("accumulate needs dT")
+    raw, ctx = _book_stream(dY.device, stream)
+    with ctx:
+        if dT is None:
+            dT = torch.empty(shape, dtype=dtype or torch.float32, device=dY.device)
+        _need(dT, "dT", dtype or dT.dtype, shape, dY.device)
+        ws, nws = _book_workspace(workspace, lambda: lib.fk_lookup_grad_workspace(B, N, D, dt, K), dY.device)
+        _check(lib.fk_lookup_grad(dY.data_ptr(), B, N, D, dt, ids.data_ptr(), K, scale, dT.data_ptr(), _dtype(dT),
+                                  int(bool(accumulate)), _addr(ws), nws, raw))
+    return dT
+
+
+def fk_balance(Z, ids, mask=None, coef=1.0, loss=None, counts=None, tokens=None, meanp=None, lse=None, workspace=None,
+               stream=None):
+    """Balance loss of the logits Z (N x E, or B x N x E: one loss per problem)
+    with the chosen columns ids (N, or N x M for M choices; B x N (x M)).
+    ``mask`` (bool or uint8, N or B x N) leaves padded rows out.  Returns (loss, counts,
+    tokens, meanp, lse); the last four are what ``fk_balance_grad`` and a
+    capacity limit need."""
+    B, N, E, bat = _dims(Z)
+    lead, top = ((B, N), (B,)) if bat else ((N,), ())
+    dev = Z.device
+    dt = _dtype(Z)
+    M = 1 if ids.dim() == len(lead) else ids.shape[-1]
+    _need(Z, "Z", Z.dtype, Z.shape, dev)
+    _need(ids, "ids", torch.int32, lead if ids.dim() == len(lead) else lead + (M,), dev)
+    if mask is not None:
+        _need(mask, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool, lead, dev)
+    raw, ctx = _book_stream(dev, stream)
+    with ctx:
+        def out(t, name, dtype, shape):
+            if t is None:
+                return torch.empty(shape, dtype=dtype, device=dev)
+            _need(t, name, dtype, shape, dev)
+            return t
+        loss = out(loss, "loss", torch.float32, top)
+        counts = out(counts, "counts", torch.int32, top + (E,))
+        tokens = out(tokens, "tokens", torch.int32, top)
+        meanp = out(meanp, "meanp", torch.float32, top + (E,))
+        lse = out(lse, "lse", torch.float32, lead)
+        ws, nws = _book_workspace(workspace, lambda: lib.fk_balance_workspace(B, N, E, dt), dev)
+        _check(lib.fk_balance(Z.data_ptr(), B, N, E, dt, ids.data_ptr(), M, _addr(mask), coef, loss.data_ptr(),
+                              counts.data_ptr(), tokens.data_ptr(), meanp.data_ptr(), lse.data_ptr(), _addr(ws), nws,
+                              raw))
+    return loss, counts, tokens, meanp, lse
+
+
+def fk_balance_grad(Z, counts, tokens, lse, M, coef=1.0, gloss=None, dZ=None, stream=None):
+    """Gradient of ``fk_balance``'s loss with respect to Z (in Z's dtype), from
+    the counts, tokens and lse it returned; ``gloss`` (fp32, the shape of the
+    loss) is the loss's own gradient, 1 by default.  ``dZ`` may be Z."""
+    B, N, E, bat = _dims(Z)
+    lead, top = ((B, N), (B,)) if bat else ((N,), ())
+    dev = Z.device
+    _need(Z, "Z", Z.dtype, Z.shape, dev)
+    _need(counts, "counts", torch.int32, top + (E,), dev)
+    _need(tokens, "tokens", torch.int32, top, dev)
+    _need(lse, "lse", torch.float32, lead, dev)
+    if gloss is not None:
+        _need(gloss, "gloss", torch.float32, top, dev)
+    raw, ctx = _book_stream(dev, stream)
+    with ctx:
+        if dZ is None:
+            dZ = torch.empty_like(Z)
+        _need(dZ, "dZ", Z.dtype, Z.shape, dev)
+        _check(lib.fk_balance_grad(Z.data_ptr(), B, N, E, _dtype(Z), counts.data_ptr(), tokens.data_ptr(),
+                                   lse.data_ptr(), M, coef, _addr(gloss), dZ.data_ptr(), raw))
+    return dZ
 
 
 def fk_sync(stream=None) -> None:

@@ -57,6 +57,9 @@ struct Scratch {
   // near-tie list counters of the assignment kernels (count, done), zeroed
   // once on allocation; the re-decision kernel leaves them zero
   int *ties_ctl = nullptr;
+  // scratch of the codebook calls (lookup gradient, balance loss)
+  void *book = nullptr;
+  size_t book_bytes = 0;
   // out-of-core driver: side copy stream and ring events, created on first use
   cudaStream_t copy = nullptr;
   cudaEvent_t ready[2] = {nullptr, nullptr}, freed[2] = {nullptr, nullptr};
@@ -64,6 +67,7 @@ struct Scratch {
 
 struct DevState {
   std::mutex mu;
+  std::mutex book_mu;  // held while a codebook call enqueues kernels that share the library's scratch
   bool ready = false;
   int sms = 0;
   int *status = nullptr;
@@ -134,6 +138,76 @@ static fk_status aux_scratch(DevState &d, cudaStream_t s, size_t need, void **ou
     w.aux_bytes = want;
   }
   *out = w.aux;
+  return FK_OK;
+}
+
+// Whether `s` is being captured into a graph; an error of the query is returned.
+static fk_status capturing(cudaStream_t s, bool *yes) {
+  cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &c);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "cudaStreamIsCapturing");
+  }
+  *yes = c != cudaStreamCaptureStatusNone;
+  return FK_OK;
+}
+
+// device_state for a call that may be captured: the first call on a device
+// allocates the status word, which a capture does not allow.
+static fk_status device_state_captured(cudaStream_t s, DevState **out) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return fail(FK_ERR_UNSUPPORTED, "device index out of range");
+  bool ready;
+  {
+    std::lock_guard<std::mutex> g(g_dev[dev].mu);
+    ready = g_dev[dev].ready;
+  }
+  if (!ready) {
+    bool cap = false;
+    const fk_status st = capturing(s, &cap);
+    if (st != FK_OK) return st;
+    if (cap) return fail(FK_ERR_UNSUPPORTED, "the first call on a device cannot be captured into a graph");
+  }
+  return device_state(out);
+}
+
+// Scratch of a codebook call: the caller's (checked against `need`), or the
+// library's for (device, stream).  The library's may be freed when a later
+// call needs more, so a captured call, whose graph would keep the address,
+// has to bring its own.
+static fk_status book_scratch(DevState &d, cudaStream_t s, size_t need, void *ws, int64_t ws_bytes, void **out) {
+  if (ws) {
+    if (ws_bytes < 0 || (size_t)ws_bytes < need)
+      return fail(FK_ERR_INVALID_ARG, "workspace of " + std::to_string(ws_bytes) + " bytes; the call needs " +
+                                          std::to_string(need));
+    if ((uintptr_t)ws % 256 != 0) return fail(FK_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+    *out = ws;
+    return FK_OK;
+  }
+  bool cap = false;
+  const fk_status st = capturing(s, &cap);
+  if (st != FK_OK) return st;
+  if (cap) return fail(FK_ERR_UNSUPPORTED, "a call captured into a graph needs the caller's workspace");
+  std::lock_guard<std::mutex> g(d.mu);
+  Scratch &w = d.scratch[s];
+  if (w.book_bytes < need) {
+    if (inject_fires(2)) return fail(FK_ERR_OOM, "scratch allocation failed (injected by fk_debug_inject)");
+    if (w.book) cudaFreeAsync(w.book, s);
+    w.book = nullptr;
+    w.book_bytes = 0;
+    const size_t want = need + need / 4 + 4096;
+    cudaError_t e = cudaMallocAsync(&w.book, want, s);
+    if (e != cudaSuccess) {
+      w.book = nullptr;
+      cudaGetLastError();
+      return cuda_fail(e, "cudaMallocAsync(scratch)");
+    }
+    w.book_bytes = want;
+  }
+  *out = w.book;
   return FK_OK;
 }
 
@@ -290,7 +364,7 @@ static fk_status read_status(DevState &d, cudaStream_t s) {
   if (h != 0) {
     cudaMemset(d.status, 0, sizeof(int));
     return fail((fk_status)h, h == FK_ERR_TIMEOUT ? "a device-side wait exceeded its time limit"
-                              : h == FK_ERR_BAD_LABEL ? "a label outside [0, K) was given to the update"
+                              : h == FK_ERR_BAD_LABEL ? "a label outside [0, K) was given to the update or to a codebook call"
                                                       : "device-side error");
   }
   return FK_OK;
@@ -749,6 +823,139 @@ fk_status fk_seed_kmeanspp(const void *X, int64_t N, int D, fk_dtype dt, int K, 
   return read_status(*d, s);
 }
 
+// Sizes of the codebook calls: `width` is D or E, at most `widest`.
+static fk_status check_book(int B, int64_t N, int width, const char *name, int widest, int64_t K, fk_dtype dt) {
+  if (!valid_dtype(dt)) return fail(FK_ERR_INVALID_ARG, "unknown dtype");
+  if (B < 1 || B > 65535) return fail(FK_ERR_INVALID_ARG, "B must be in [1, 65535]");
+  if (N < 0) return fail(FK_ERR_INVALID_ARG, "N must be >= 0");
+  if (width < 1 || width > widest)
+    return fail(FK_ERR_INVALID_ARG, std::string(name) + " must be in [1, " + std::to_string(widest) + "]");
+  if (K < 1) return fail(FK_ERR_INVALID_ARG, "K must be >= 1");
+  if (N >= (1ll << 31) || (long long)B * N >= (1ll << 31)) return fail(FK_ERR_INVALID_ARG, "B*N must be < 2^31");
+  if ((long long)B * K >= (1ll << 22)) return fail(FK_ERR_INVALID_ARG, "B*K must be < 2^22");
+  return FK_OK;
+}
+// What an entry point returns when the host runs out of memory inside it.
+static fk_status thrown() {
+  t_last = FK_ERR_OOM;
+  t_msg.clear();
+  return FK_ERR_OOM;
+}
+static bool finite_f(float v) { return v - v == 0.f; }
+
+fk_status fk_lookup(const void *T, int B, int K, int D, fk_dtype dt, const int32_t *ids, int64_t N, float scale,
+                    void *Y, fk_dtype dt_y, fk_stream_t stream) try {
+  fk_status st = check_book(B, N, D, "D", kMaxLookupD, K, dt);
+  if (st != FK_OK) return st;
+  if (!valid_dtype(dt_y)) return fail(FK_ERR_INVALID_ARG, "unknown dtype of Y");
+  if (!finite_f(scale)) return fail(FK_ERR_INVALID_ARG, "scale must be finite");
+  if (N == 0) return FK_OK;
+  if (!T || !ids || !Y) return fail(FK_ERR_INVALID_ARG, "T, ids and Y must not be NULL");
+  DevState *d;
+  cudaStream_t s = (cudaStream_t)stream;
+  if ((st = device_state_captured(s, &d)) != FK_OK) return st;
+  const LookupArgs a{T, ids, Y, B, (int)N, K, D, (DType)dt, (DType)dt_y, scale};
+  const cudaError_t e = launch_lookup(a, d->status, s);
+  return e == cudaSuccess ? FK_OK : cuda_fail(e, "lookup kernel");
+} catch (...) {
+  return thrown();
+}
+
+int64_t fk_lookup_grad_workspace(int B, int64_t N, int D, fk_dtype dt, int K) try {
+  const fk_status st = check_book(B, N, D, "D", kMaxLookupD, K, dt);
+  if (st != FK_OK) return st;
+  return N == 0 ? 0 : (int64_t)lookup_grad_workspace_bytes((int64_t)B * N, (int64_t)B * K, B, D, (DType)dt);
+} catch (...) {
+  return thrown();
+}
+
+fk_status fk_lookup_grad(const void *dY, int B, int64_t N, int D, fk_dtype dt, const int32_t *ids, int K, float scale,
+                         void *dT, fk_dtype dt_t, int accumulate, void *ws, int64_t ws_bytes, fk_stream_t stream) try {
+  fk_status st = check_book(B, N, D, "D", kMaxLookupD, K, dt);
+  if (st != FK_OK) return st;
+  if (!valid_dtype(dt_t)) return fail(FK_ERR_INVALID_ARG, "unknown dtype of dT");
+  if (!finite_f(scale)) return fail(FK_ERR_INVALID_ARG, "scale must be finite");
+  if (accumulate != 0 && accumulate != 1) return fail(FK_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  if (!dT) return fail(FK_ERR_INVALID_ARG, "dT must not be NULL");
+  if (N > 0 && (!dY || !ids)) return fail(FK_ERR_INVALID_ARG, "dY and ids must not be NULL");
+  DevState *d;
+  cudaStream_t s = (cudaStream_t)stream;
+  if ((st = device_state_captured(s, &d)) != FK_OK) return st;
+  const LookupGradArgs a{dY, ids, dT, B, (int)N, K, D, (DType)dt, (DType)dt_t, scale, accumulate};
+  std::lock_guard<std::mutex> g(d->book_mu);
+  void *work = nullptr;
+  if (N > 0) {
+    const size_t need = lookup_grad_workspace_bytes((int64_t)B * N, (int64_t)B * K, B, D, (DType)dt);
+    if ((st = book_scratch(*d, s, need, ws, ws_bytes, &work)) != FK_OK) return st;
+  }
+  const cudaError_t e = launch_lookup_grad(a, work, d->status, s);
+  return e == cudaSuccess ? FK_OK : cuda_fail(e, "lookup gradient kernels");
+} catch (...) {
+  return thrown();
+}
+
+int64_t fk_balance_workspace(int B, int64_t N, int E, fk_dtype dt) try {
+  const fk_status st = check_book(B, N, E, "E", kMaxBalanceE, 1, dt);
+  if (st != FK_OK) return st;
+  return N == 0 ? 0 : (int64_t)balance_workspace_bytes(B, N, E, (DType)dt);
+} catch (...) {
+  return thrown();
+}
+
+static fk_status check_balance(int B, int64_t N, int E, fk_dtype dt, int M, float coef) {
+  const fk_status st = check_book(B, N, E, "E", kMaxBalanceE, 1, dt);
+  if (st != FK_OK) return st;
+  if (M < 1 || M > 64) return fail(FK_ERR_INVALID_ARG, "M must be in [1, 64]");
+  if ((long long)B * N * M >= (1ll << 31)) return fail(FK_ERR_INVALID_ARG, "B*N*M must be < 2^31");
+  if (!finite_f(coef)) return fail(FK_ERR_INVALID_ARG, "coef must be finite");
+  return FK_OK;
+}
+
+fk_status fk_balance(const void *Z, int B, int64_t N, int E, fk_dtype dt, const int32_t *ids, int M,
+                     const uint8_t *mask, float coef, float *loss, int32_t *counts, int32_t *tokens, float *meanp,
+                     float *lse, void *ws, int64_t ws_bytes, fk_stream_t stream) try {
+  fk_status st = check_balance(B, N, E, dt, M, coef);
+  if (st != FK_OK) return st;
+  if (!loss || !counts || !tokens) return fail(FK_ERR_INVALID_ARG, "loss, counts and tokens must not be NULL");
+  cudaStream_t s = (cudaStream_t)stream;
+  if (N == 0) {  // no row takes part: every result is 0
+    cudaError_t e = cudaMemsetAsync(loss, 0, (size_t)B * 4, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, (size_t)B * E * 4, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, (size_t)B * 4, s);
+    if (e == cudaSuccess && meanp) e = cudaMemsetAsync(meanp, 0, (size_t)B * E * 4, s);
+    return e == cudaSuccess ? FK_OK : cuda_fail(e, "cudaMemsetAsync");
+  }
+  if (!Z || !ids) return fail(FK_ERR_INVALID_ARG, "Z and ids must not be NULL");
+  DevState *d;
+  if ((st = device_state_captured(s, &d)) != FK_OK) return st;
+  std::lock_guard<std::mutex> g(d->book_mu);
+  void *work = nullptr;
+  if ((st = book_scratch(*d, s, balance_workspace_bytes(B, N, E, (DType)dt), ws, ws_bytes, &work)) != FK_OK) return st;
+  const BalanceArgs a{Z, ids, mask, B, (int)N, E, M, (DType)dt, coef, loss, counts, tokens, meanp, lse};
+  const cudaError_t e = launch_balance(a, work, d->status, s);
+  return e == cudaSuccess ? FK_OK : cuda_fail(e, "balance kernels");
+} catch (...) {
+  return thrown();
+}
+
+fk_status fk_balance_grad(const void *Z, int B, int64_t N, int E, fk_dtype dt, const int32_t *counts,
+                          const int32_t *tokens, const float *lse, int M, float coef, const float *gloss, void *dZ,
+                          fk_stream_t stream) try {
+  fk_status st = check_balance(B, N, E, dt, M, coef);
+  if (st != FK_OK) return st;
+  if (N == 0) return FK_OK;
+  if (!Z || !counts || !tokens || !lse || !dZ)
+    return fail(FK_ERR_INVALID_ARG, "Z, counts, tokens, lse and dZ must not be NULL");
+  DevState *d;
+  cudaStream_t s = (cudaStream_t)stream;
+  if ((st = device_state_captured(s, &d)) != FK_OK) return st;
+  const BalanceGradArgs a{Z, counts, tokens, lse, gloss, B, (int)N, E, M, (DType)dt, coef, dZ};
+  const cudaError_t e = launch_balance_grad(a, s);
+  return e == cudaSuccess ? FK_OK : cuda_fail(e, "balance gradient kernel");
+} catch (...) {
+  return thrown();
+}
+
 fk_status fk_sync(fk_stream_t stream) {
   DevState *d;
   fk_status st = device_state(&d);
@@ -812,6 +1019,7 @@ fk_status fk_release_workspace(void) {
   for (auto &kv : d->scratch) {
     if (kv.second.ptr) cudaFreeAsync(kv.second.ptr, kv.first);
     if (kv.second.aux) cudaFreeAsync(kv.second.aux, kv.first);
+    if (kv.second.book) cudaFreeAsync(kv.second.book, kv.first);
     if (kv.second.ties_ctl) cudaFreeAsync(kv.second.ties_ctl, kv.first);
   }
   cudaError_t e = cudaDeviceSynchronize();

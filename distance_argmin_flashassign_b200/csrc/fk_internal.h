@@ -131,6 +131,57 @@ size_t label_sort_bytes(int64_t Ntot, int64_t Ktot, int B, bool drop);
 cudaError_t launch_label_sort(const int32_t *labels, int B, int N, int K, bool drop, void *ws, int *status,
                               cudaStream_t s, LabelSort *out);
 
+// ---- lookup.cu: codebook rows by label, and the codebook's gradient --------
+constexpr int kMaxLookupD = 16384;  // largest D of these calls
+struct LookupArgs {
+  const void *T;       // B x K rows of D elements of dt
+  const int32_t *ids;  // B x N
+  void *Y;             // B x N rows of D elements of dt_y
+  int B, N, K, D;
+  DType dt, dt_y;
+  float scale;
+};
+cudaError_t launch_lookup(const LookupArgs &a, int *status, cudaStream_t s);
+struct LookupGradArgs {
+  const void *dY;      // B x N rows of D elements of dt
+  const int32_t *ids;  // B x N
+  void *dT;            // B x K rows of D elements of dt_t
+  int B, N, K, D;
+  DType dt, dt_t;
+  float scale;
+  int accumulate;  // add to dT; else rows without a label are zeroed
+};
+size_t lookup_grad_workspace_bytes(int64_t rows, int64_t Ktot, int B, int D, DType dt);
+cudaError_t launch_lookup_grad(const LookupGradArgs &a, void *ws, int *status, cudaStream_t s);
+
+// ---- balance.cu: balance loss of routed rows --------------------------------
+constexpr int kMaxBalanceE = 8192;  // largest E
+struct BalanceArgs {
+  const void *Z;        // B x N rows of E logits of dt
+  const int32_t *ids;   // B x N x M chosen columns, -1: none
+  const uint8_t *mask;  // B x N, 0: the row takes no part; or null
+  int B, N, E, M;
+  DType dt;
+  float coef;
+  float *loss;      // B
+  int32_t *counts;  // B x E
+  int32_t *tokens;  // B
+  float *meanp;     // B x E or null
+  float *lse;       // B x N or null
+};
+size_t balance_workspace_bytes(int B, int64_t N, int E, DType dt);
+cudaError_t launch_balance(const BalanceArgs &a, void *ws, int *status, cudaStream_t s);
+struct BalanceGradArgs {
+  const void *Z;
+  const int32_t *counts, *tokens;
+  const float *lse, *gloss;  // gloss: B, or null (1)
+  int B, N, E, M;
+  DType dt;
+  float coef;
+  void *dZ;
+};
+cudaError_t launch_balance_grad(const BalanceGradArgs &a, cudaStream_t s);
+
 // ---- update.cu: sort-inverse update ---------------------------------------
 enum UpdateMode : int { kMean = 0, kAccumulate = 1 };
 struct UpdateArgs {

@@ -1,0 +1,352 @@
+// lookup.cu -- rows of a codebook by label, and the codebook's gradient.
+//
+//   Y[b,i]  = scale T[b, ids[b,i]]                    (fk_lookup)
+//   dT[b,k] = scale sum over ids[b,i] = k of dY[b,i]  (fk_lookup_grad)
+//
+// The lookup is the assignment's inverse (points replaced by the centroids
+// their labels name); its gradient is the sum part of the centroid update and
+// runs on the same sorted order (label_sort.cu): no atomics, every sum in one
+// fixed order.  A label of -1 names no row: a zero row of Y, no part in dT.
+#include <type_traits>
+
+#include "chain.cuh"
+#include "fk_internal.h"
+
+namespace fk {
+
+// ---------------------------------------------------------------- vectors --
+// VB bytes moved by one instruction.
+template <int VB> struct Raw;
+template <> struct Raw<16> { using type = uint4; };
+template <> struct Raw<8> { using type = uint2; };
+template <> struct Raw<4> { using type = unsigned int; };
+template <> struct Raw<2> { using type = unsigned short; };
+
+template <int VB> __device__ __forceinline__ typename Raw<VB>::type ld_raw(const void *p) {
+  return __ldg(reinterpret_cast<const typename Raw<VB>::type *>(p));
+}
+template <typename T, int VB> __device__ __forceinline__ void unpack_raw(const typename Raw<VB>::type &r, float *v) {
+  constexpr int n = VB / (int)sizeof(T);
+  T e[n];
+  memcpy(e, &r, VB);
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = to_f32<T>(e[i]);
+}
+// n values rounded to nearest even and stored as one vector.
+template <typename T, int n> __device__ __forceinline__ void st_vec(T *p, const float *v) {
+  constexpr int VB = n * (int)sizeof(T);
+  if constexpr (VB > 16) {
+    st_vec<T, n / 2>(p, v);
+    st_vec<T, n / 2>(p + n / 2, v + n / 2);
+  } else {
+    T e[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) e[i] = from_f32<T>(v[i]);
+    typename Raw<VB>::type r;
+    memcpy(&r, e, VB);
+    *reinterpret_cast<typename Raw<VB>::type *>(p) = r;
+  }
+}
+template <typename T, int n> __device__ __forceinline__ void ld_vec(const T *p, float *v) {
+  constexpr int VB = n * (int)sizeof(T);
+  if constexpr (VB > 16) {
+    ld_vec<T, n / 2>(p, v);
+    ld_vec<T, n / 2>(p + n / 2, v + n / 2);
+  } else {
+    const typename Raw<VB>::type r = *reinterpret_cast<const typename Raw<VB>::type *>(p);
+    unpack_raw<T, VB>(r, v);
+  }
+}
+
+// ----------------------------------------------------------------- lookup --
+constexpr int kLookRows = 4;  // rows in flight per group of lanes
+// Groups of W = 2^logw lanes, one row each; lane l of a group moves EPL
+// elements of column slice blockIdx.y.
+template <typename TI, typename TO, int EPL>
+__global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ T, int K, int D,
+                                                     const int32_t *__restrict__ ids, long long rows, int N, int B,
+                                                     float scale, TO *__restrict__ Y, int logw, int *status) {
+  constexpr int VB = EPL * (int)sizeof(TI);
+  const int lane = threadIdx.x & 31;
+  const int col = ((blockIdx.y << logw) + (lane & ((1 << logw) - 1))) * EPL;
+  const int per = 32 >> logw;  // rows of a warp's step
+  const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long r0 = warp * (kLookRows * per) + (lane >> logw);
+  if (col >= D) return;
+  typename Raw<VB>::type v[kLookRows];
+  bool have[kLookRows], bad = false;
+#pragma unroll
+  for (int u = 0; u < kLookRows; ++u) {
+    const long long r = r0 + u * per;
+    const int id = r < rows ? __ldg(ids + r) : -1;
+    have[u] = (unsigned)id < (unsigned)K;
+    bad |= !have[u] && id != -1;
+    if (have[u]) {
+      const long long b = B > 1 ? r / N : 0;
+      v[u] = ld_raw<VB>(T + (size_t)(b * K + id) * D + col);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kLookRows; ++u) {
+    const long long r = r0 + u * per;
+    if (r >= rows) break;
+    float f[EPL];
+    if (have[u]) {
+      unpack_raw<TI, VB>(v[u], f);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) f[i] *= scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) f[i] = 0.f;
+    }
+    st_vec<TO, EPL>(Y + (size_t)r * D + col, f);
+  }
+  if (bad) record_status(status, kStBadLabel);
+}
+
+template <typename TI, typename TO, int EPL>
+static void launch_lookup_as(const LookupArgs &a, int *status, cudaStream_t s) {
+  const int vecs = a.D / EPL;
+  int logw = 0;
+  while (logw < 5 && (1 << logw) < vecs) ++logw;
+  const int slices = (vecs + (1 << logw) - 1) >> logw;
+  const long long rows = (long long)a.B * a.N, per_block = 8ll * kLookRows * (32 >> logw);
+  lookup_kernel<TI, TO, EPL><<<dim3((unsigned)((rows + per_block - 1) / per_block), slices), 256, 0, s>>>(
+      (const TI *)a.T, a.K, a.D, a.ids, rows, a.N, a.B, a.scale, (TO *)a.Y, logw, status);
+}
+template <typename TI, typename TO> static void launch_lookup_to(const LookupArgs &a, int *status, cudaStream_t s) {
+  constexpr int widest = 16 / (int)(sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO));
+  auto fits = [&](int n) {
+    return a.D % n == 0 && (uintptr_t)a.T % (n * sizeof(TI)) == 0 && (uintptr_t)a.Y % (n * sizeof(TO)) == 0;
+  };
+  if (fits(widest)) launch_lookup_as<TI, TO, widest>(a, status, s);
+  else if (fits(2)) launch_lookup_as<TI, TO, 2>(a, status, s);
+  else launch_lookup_as<TI, TO, 1>(a, status, s);
+}
+template <typename TI> static void launch_lookup_from(const LookupArgs &a, int *status, cudaStream_t s) {
+  if (a.dt_y == kF32) launch_lookup_to<TI, float>(a, status, s);
+  else if (a.dt_y == kF16) launch_lookup_to<TI, __half>(a, status, s);
+  else launch_lookup_to<TI, __nv_bfloat16>(a, status, s);
+}
+cudaError_t launch_lookup(const LookupArgs &a, int *status, cudaStream_t s) {
+  if (a.dt == kF32) launch_lookup_from<float>(a, status, s);
+  else if (a.dt == kF16) launch_lookup_from<__half>(a, status, s);
+  else launch_lookup_from<__nv_bfloat16>(a, status, s);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// --------------------------------------------------------------- gradient --
+// Sorted positions per worker, from the number of 16-byte pieces of dY alone,
+// so that the order of a sum depends on the sizes and on nothing else.
+// 148 SMs hold 113,664 lanes of the row-sum kernel (3 blocks of 256).
+static int grad_rows_R(long long rows, int row_bytes) {
+  const long long pieces = rows * ((row_bytes + 15) / 16);
+  long long R = (pieces + 113663) / 113664;
+  R = (R + 7) / 8 * 8;
+  return (int)(R < 32 ? 32 : R > 512 ? 512 : R);
+}
+
+// Writes scale v (+ the row's own values) at columns [col, col + n) of row k.
+template <int n>
+__device__ __forceinline__ void put_grad(void *dT, int dt, size_t at, float *v, float scale, bool add) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] *= scale;
+  float o[n];
+  if (dt == kF32) {
+    float *p = (float *)dT + at;
+    if (add) {
+      ld_vec<float, n>(p, o);
+#pragma unroll
+      for (int i = 0; i < n; ++i) v[i] += o[i];
+    }
+    st_vec<float, n>(p, v);
+  } else if (dt == kF16) {
+    __half *p = (__half *)dT + at;
+    if (add) {
+      ld_vec<__half, n>(p, o);
+#pragma unroll
+      for (int i = 0; i < n; ++i) v[i] += o[i];
+    }
+    st_vec<__half, n>(p, v);
+  } else {
+    __nv_bfloat16 *p = (__nv_bfloat16 *)dT + at;
+    if (add) {
+      ld_vec<__nv_bfloat16, n>(p, o);
+#pragma unroll
+      for (int i = 0; i < n; ++i) v[i] += o[i];
+    }
+    st_vec<__nv_bfloat16, n>(p, v);
+  }
+}
+
+// Worker = W lanes, one chunk of R sorted positions and one slice of W * EPL
+// columns.  A segment (run of one label) inside the chunk goes straight to
+// dT; the pieces of segments that cross the chunk's ends go to the chunk's
+// two partial rows (0: the piece that starts the chunk, 1: the one that ends
+// it).  `none` is the key of the points left out.
+constexpr int kGradRows = 8;  // rows in flight per worker
+template <typename T, int VB, int W>
+__global__ void __launch_bounds__(256, 3) grad_sum_kernel(const T *__restrict__ dY, int D,
+                                                          const int32_t *__restrict__ skeys,
+                                                          const int32_t *__restrict__ perm, int rows, int none, int R,
+                                                          float scale, void *__restrict__ dT, int dt_t, int add,
+                                                          float *__restrict__ parts) {
+  constexpr int EPL = VB / (int)sizeof(T), U = kGradRows;
+  const int lw = threadIdx.x % W;
+  const int col = (blockIdx.y * W + lw) * EPL;
+  const bool mine = col < D;
+  const long long wq = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
+  wait_prior_grid();
+  const long long p0l = wq * R;
+  const int p0 = p0l < rows ? (int)p0l : rows;
+  const int p1 = rows - p0 < R ? rows : p0 + R;
+  const bool live = p0 < p1;
+  int cur = live ? skeys[p0] : none, s = p0;
+  const bool split_start = live && p0 > 0 && skeys[p0 - 1] == cur;
+  const bool split_end = live && p1 < rows && skeys[p1] == skeys[p1 - 1];
+  float a[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) a[i] = 0.f;
+  auto flush = [&](int k, int sb, int se) {
+    if (k == none || !mine) return;
+    if ((sb == p0 && split_start) || (se == p1 && split_end))
+      st_vec<float, EPL>(parts + ((size_t)wq * 2 + (sb == p0 ? 0 : 1)) * D + col, a);
+    else
+      put_grad<EPL>(dT, dt_t, (size_t)k * D + col, a, scale, add);
+  };
+  const int nb = (R + U - 1) / U;  // the same for every worker: shuffles stay converged
+  for (int bt = 0; bt < nb; ++bt) {
+    const int b0 = p0 + bt * U;
+    const bool in = lw < U && b0 + lw < p1;
+    const int mk = in ? skeys[b0 + lw] : none, mr = in ? perm[b0 + lw] : 0;
+    typename Raw<VB>::type v[U];
+    int ku[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = __shfl_sync(0xffffffffu, mr, u, W);
+      ku[u] = __shfl_sync(0xffffffffu, mk, u, W);
+      if (ku[u] != none && mine) v[u] = ld_raw<VB>(dY + (size_t)row * D + col);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + u >= p1) break;
+      if (ku[u] != cur) {
+        flush(cur, s, b0 + u);
+        cur = ku[u];
+        s = b0 + u;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) a[i] = 0.f;
+      }
+      if (cur != none && mine) {
+        float f[EPL];
+        unpack_raw<T, VB>(v[u], f);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) a[i] += f[i];
+      }
+    }
+  }
+  if (live) flush(cur, s, p1);
+}
+
+// One block per chunk and 128 columns: if a segment starts in this chunk and
+// runs past its end, its partial rows are added -- warp w takes pieces w,
+// w + 8, ..., then the eight sums in warp order -- and written.
+__global__ void __launch_bounds__(256) grad_join_kernel(const int32_t *__restrict__ skeys, int rows, int none, int R,
+                                                        int D, const float *__restrict__ parts, float scale,
+                                                        void *__restrict__ dT, int dt_t, int add) {
+  __shared__ float red[8][128];
+  wait_prior_grid();
+  const int q = blockIdx.x, p0 = q * R;
+  if (rows - p0 <= R) return;  // the last chunk: nothing runs past it
+  const int p1 = p0 + R, k = skeys[p1 - 1];
+  if (k == none || skeys[p1] != k) return;
+  if (p0 > 0 && skeys[p0 - 1] == k) return;  // started in an earlier chunk
+  const int first = skeys[p0] == k ? 0 : 1;
+  const int nchunks = (rows + R - 1) / R;
+  // pieces: this chunk's and those of the following chunks that start with k
+  // (a label's positions are consecutive, so these chunks are too)
+  int np = 1;
+  for (int more = 256; more == 256; np += more) {
+    const int i = q + np + (int)threadIdx.x;
+    more = __syncthreads_count(i < nchunks && skeys[i < nchunks ? i * R : 0] == k);
+  }
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c0 = blockIdx.y * 128;
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = w; i < np; i += 8) {
+    const float *row = parts + ((size_t)(q + i) * 2 + (i == 0 ? first : 0)) * D + c0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c0 + lane + 32 * j < D) t[j] += row[lane + 32 * j];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) red[w][lane + 32 * j] = t[j];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < 128 && c0 + c < D) {
+    float sum[1] = {0.f};
+    for (int ww = 0; ww < 8; ++ww) sum[0] += red[ww][c];
+    put_grad<1>(dT, dt_t, (size_t)k * D + c0 + c, sum, scale, add);
+  }
+}
+
+static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
+
+size_t lookup_grad_workspace_bytes(int64_t rows, int64_t Ktot, int B, int D, DType dt) {
+  const int R = grad_rows_R(rows, D * (int)dtype_size(dt));
+  return al256(label_sort_bytes(rows, Ktot, B, true)) + al256((size_t)((rows + R - 1) / R) * 2 * D * sizeof(float));
+}
+
+template <typename T, int VB, int W>
+static void launch_grad_sum(const LookupGradArgs &a, const LabelSort &o, int rows, int none, int R, float *parts,
+                            cudaStream_t s) {
+  constexpr int EPL = VB / (int)sizeof(T);
+  const long long chunks = ((long long)rows + R - 1) / R;
+  const dim3 grid((unsigned)((chunks * W + 255) / 256), (a.D + W * EPL - 1) / (W * EPL));
+  launch_chained(grad_sum_kernel<T, VB, W>, grid, dim3(256), 0, s, (const T *)a.dY, a.D, o.skeys, o.perm, rows, none, R,
+                 a.scale, a.dT, (int)a.dt_t, a.accumulate, parts);
+}
+template <typename T>
+static void launch_grad_from(const LookupGradArgs &a, const LabelSort &o, int rows, int none, int R, float *parts,
+                             cudaStream_t s) {
+  // the widest vector that the row length and both pointers allow
+  auto fits = [&](int vb) {
+    const int n = vb / (int)sizeof(T), out = n * (int)dtype_size(a.dt_t);
+    return a.D % n == 0 && (uintptr_t)a.dY % vb == 0 && (uintptr_t)a.dT % (out < 16 ? out : 16) == 0;
+  };
+  if (fits(16)) {
+    const int vecs = a.D * (int)sizeof(T) / 16;
+    if (vecs <= 8) launch_grad_sum<T, 16, 8>(a, o, rows, none, R, parts, s);
+    else if (vecs <= 16) launch_grad_sum<T, 16, 16>(a, o, rows, none, R, parts, s);
+    else launch_grad_sum<T, 16, 32>(a, o, rows, none, R, parts, s);
+  } else if (fits(8)) {
+    launch_grad_sum<T, 8, 32>(a, o, rows, none, R, parts, s);
+  } else if (sizeof(T) == 4 || fits(4)) {
+    launch_grad_sum<T, 4, 32>(a, o, rows, none, R, parts, s);
+  } else if constexpr (sizeof(T) == 2) {
+    launch_grad_sum<T, 2, 32>(a, o, rows, none, R, parts, s);
+  }
+}
+
+cudaError_t launch_lookup_grad(const LookupGradArgs &a, void *ws, int *status, cudaStream_t s) {
+  const long long rows = (long long)a.B * a.N, Ktot = (long long)a.B * a.K;
+  if (!a.accumulate) {
+    cudaError_t e = cudaMemsetAsync(a.dT, 0, (size_t)Ktot * a.D * dtype_size(a.dt_t), s);
+    if (e != cudaSuccess) return e;
+  }
+  if (rows == 0) return cudaSuccess;
+  LabelSort o;
+  cudaError_t e = launch_label_sort(a.ids, a.B, a.N, a.K, true, ws, status, s, &o);
+  if (e != cudaSuccess) return e;
+  float *parts = (float *)((char *)ws + al256(label_sort_bytes(rows, Ktot, a.B, true)));
+  const int R = grad_rows_R(rows, a.D * (int)dtype_size(a.dt)), none = (int)Ktot, n = (int)rows;
+  if (a.dt == kF32) launch_grad_from<float>(a, o, n, none, R, parts, s);
+  else if (a.dt == kF16) launch_grad_from<__half>(a, o, n, none, R, parts, s);
+  else launch_grad_from<__nv_bfloat16>(a, o, n, none, R, parts, s);
+  launch_chained(grad_join_kernel, dim3((n + R - 1) / R, (a.D + 127) / 128), dim3(256), 0, s, o.skeys, n, none, R, a.D,
+                 parts, a.scale, a.dT, (int)a.dt_t, a.accumulate);
+  count_launches(2);
+  return cudaGetLastError();
+}
+
+}  // namespace fk

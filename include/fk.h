@@ -97,7 +97,7 @@ enum {
   FK_ERR_OOM = -4,         /* device or pinned allocation failed               */
   FK_ERR_TIMEOUT = -5,     /* a device-side wait exceeded its time limit       */
   FK_ERR_HOST_IO = -6,     /* a host<->device copy failed (out-of-core path)   */
-  FK_ERR_BAD_LABEL = -7    /* fk_update saw a label outside [0, K)             */
+  FK_ERR_BAD_LABEL = -7    /* a label outside [0, K) (fk_update, codebook calls) */
 };
 
 /* ------------------------------------------------------------------------
@@ -353,6 +353,94 @@ FK_API fk_status fk_gauss_sum(const void *X, int64_t N, int D, fk_dtype dt, cons
  * ------------------------------------------------------------------------ */
 FK_API fk_status fk_seed_kmeanspp(const void *X, int64_t N, int D, fk_dtype dt, int K, const double *u,
                                   int32_t *centers, fk_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Codebook calls -- what a model does with the labels: the rows they name,
+ * the gradient of those rows' table, and a loss on how evenly the columns
+ * are chosen.  (The pages name vector quantisation and sparse routing as
+ * uses of the labels, Japanese Hacker News summary, first section; they give
+ * no operator for them.)  Conventions as above, with these differences:
+ *   Limits     1 <= D <= 16384; 1 <= E <= 8192; 1 <= M <= 64;
+ *              B*K < 2^22; B*N < 2^31; B*N*M < 2^31.
+ *   Alignment  every array aligned to its element type; rows and pointers of
+ *              whole 16 bytes run on the widest loads and stores.
+ *   Capture    the calls may be captured into a CUDA graph once a call has
+ *              been made on the device.  Those with a workspace (ws, ws_bytes)
+ *              then need the caller's: 256-byte aligned device memory of at
+ *              least the bytes that the _workspace function returns (a
+ *              negative status for invalid sizes), which two calls may share
+ *              only if they cannot overlap on the GPU.  With ws = NULL the
+ *              library's scratch for (device, stream) is used; a capture
+ *              is then refused with FK_ERR_UNSUPPORTED.
+ *   Labels     -1 names nothing (padding, a dropped choice) and is not an
+ *              error.  Any other label outside its range is treated as -1 and
+ *              reported as FK_ERR_BAD_LABEL by fk_sync().
+ * ------------------------------------------------------------------------ */
+
+/* fk_lookup -- the rows that labels name, scaled.
+ *     Y[b][i] = round(scale * T[b][ids[b][i]]),  0 for ids -1
+ *   The product is taken in fp32 and rounded once to dt_y.
+ *   T    device, B x K x D, dtype dt
+ *   ids  device, B x N int32
+ *   Y    device, B x N x D, dtype dt_y (out); must not overlap T
+ *   N may be 0.  One kernel.  Asynchronous on `stream`. */
+FK_API fk_status fk_lookup(const void *T, int B, int K, int D, fk_dtype dt, const int32_t *ids, int64_t N, float scale,
+                           void *Y, fk_dtype dt_y, fk_stream_t stream);
+
+/* fk_lookup_grad -- gradient of fk_lookup with respect to T, by sorted labels.
+ *     dT[b][k] = round(scale * sum over i with ids[b][i] = k of dY[b][i]
+ *                      (+ dT[b][k] if accumulate))
+ *   The sort-inverse sums of fk_update without the division: fp32 sums in an
+ *   order fixed by the sizes and the alignment, rounded once to dt_t, the same
+ *   bits on every run; no atomics.  Without accumulate every row is written
+ *   (zeros where no label names it); with it the rows that no label names
+ *   are left untouched.
+ *   dY   device, B x N x D, dtype dt
+ *   ids  device, B x N int32
+ *   dT   device, B x K x D, dtype dt_t (out, or in/out); must not overlap dY
+ *   Asynchronous on `stream`. */
+FK_API int64_t fk_lookup_grad_workspace(int B, int64_t N, int D, fk_dtype dt, int K);
+FK_API fk_status fk_lookup_grad(const void *dY, int B, int64_t N, int D, fk_dtype dt, const int32_t *ids, int K,
+                                float scale, void *dT, fk_dtype dt_t, int accumulate, void *ws, int64_t ws_bytes,
+                                fk_stream_t stream);
+
+/* fk_balance -- balance loss of N rows of E logits with M chosen columns each
+ * (experts of a router, codes of a codebook), and the per-column counts.
+ *   A row takes part if its mask is not 0 and some logit is above -inf (a
+ *   NaN counts as above).  For the n rows of a problem that take part:
+ *     lse_i = ln sum_e exp z_ie     p_ie = exp(z_ie - lse_i)
+ *     P_e = (1/n) sum_i p_ie        f_e = counts_e / (M n)
+ *     loss = coef * E * sum_e f_e P_e
+ *   so that even use gives coef.  n = 0 gives 0.  A dropped choice (-1) stays
+ *   in the M n of f.  A NaN or +inf logit of a row that takes part gives NaN,
+ *   as the formula does; rows that take no part are not looked at.
+ *   Z       device, B x N x E, dtype dt
+ *   ids     device, B x N x M int32, each in [0, E) or -1
+ *   mask    device, B x N bytes, or NULL (every row)
+ *   loss    device, B fp32 (out)
+ *   counts  device, B x E int32 (out)
+ *   tokens  device, B int32 (out): n
+ *   meanp   device, B x E fp32 (out): P, or NULL
+ *   lse     device, B x N fp32 (out): +inf for a row that takes no part, or
+ *           NULL; fk_balance_grad reads it
+ *   Deterministic.  Asynchronous on `stream`. */
+FK_API int64_t fk_balance_workspace(int B, int64_t N, int E, fk_dtype dt);
+FK_API fk_status fk_balance(const void *Z, int B, int64_t N, int E, fk_dtype dt, const int32_t *ids, int M,
+                            const uint8_t *mask, float coef, float *loss, int32_t *counts, int32_t *tokens,
+                            float *meanp, float *lse, void *ws, int64_t ws_bytes, fk_stream_t stream);
+
+/* fk_balance_grad -- gradient of fk_balance with respect to the logits (the
+ * counts are constants):
+ *     dZ_ie = g coef E / n * p_ie (f_e - sum_j f_j p_ij)
+ *   and 0 in the rows that took no part.  counts, tokens, lse, M and coef as
+ *   fk_balance gave or took them.
+ *   gloss  device, B fp32: the loss's own gradient g, or NULL (1)
+ *   dZ     device, B x N x E, dtype dt (out); may be Z itself, must not
+ *          overlap it otherwise
+ *   One kernel.  Asynchronous on `stream`. */
+FK_API fk_status fk_balance_grad(const void *Z, int B, int64_t N, int E, fk_dtype dt, const int32_t *counts,
+                                 const int32_t *tokens, const float *lse, int M, float coef, const float *gloss,
+                                 void *dZ, fk_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Status, diagnostics and control.
