@@ -25,12 +25,41 @@ template <> struct Raw<2> { using type = unsigned short; };
 template <int VB> __device__ __forceinline__ typename Raw<VB>::type ld_raw(const void *p) {
   return __ldg(reinterpret_cast<const typename Raw<VB>::type *>(p));
 }
+// Two 16-bit values of a word, and back (rounded to nearest even).
+template <typename T> __device__ __forceinline__ void unpack2(uint32_t w, float *v) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+  } else {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
+  }
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t w;
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(a, b);
+    memcpy(&w, &h, 4);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    memcpy(&w, &h, 4);
+  }
+  return w;
+}
 template <typename T, int VB> __device__ __forceinline__ void unpack_raw(const typename Raw<VB>::type &r, float *v) {
-  constexpr int n = VB / (int)sizeof(T);
-  T e[n];
-  memcpy(e, &r, VB);
+  if constexpr (sizeof(T) == 4) {
+    memcpy(v, &r, VB);
+  } else if constexpr (VB == 2) {
+    T e;
+    memcpy(&e, &r, 2);
+    v[0] = to_f32<T>(e);
+  } else {
+    uint32_t w[VB / 4];
+    memcpy(w, &r, VB);
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = to_f32<T>(e[i]);
+    for (int i = 0; i < VB / 4; ++i) unpack2<T>(w[i], v + 2 * i);
+  }
 }
 // n values rounded to nearest even and stored as one vector.
 template <typename T, int n> __device__ __forceinline__ void st_vec(T *p, const float *v) {
@@ -39,11 +68,18 @@ template <typename T, int n> __device__ __forceinline__ void st_vec(T *p, const 
     st_vec<T, n / 2>(p, v);
     st_vec<T, n / 2>(p + n / 2, v + n / 2);
   } else {
-    T e[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) e[i] = from_f32<T>(v[i]);
     typename Raw<VB>::type r;
-    memcpy(&r, e, VB);
+    if constexpr (sizeof(T) == 4) {
+      memcpy(&r, v, VB);
+    } else if constexpr (n == 1) {
+      const T e = from_f32<T>(v[0]);
+      memcpy(&r, &e, 2);
+    } else {
+      uint32_t w[n / 2];
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+      memcpy(&r, w, VB);
+    }
     *reinterpret_cast<typename Raw<VB>::type *>(p) = r;
   }
 }
@@ -59,60 +95,129 @@ template <typename T, int n> __device__ __forceinline__ void ld_vec(const T *p, 
 }
 
 // ----------------------------------------------------------------- lookup --
-constexpr int kLookRows = 4;  // rows in flight per group of lanes
-// Groups of W = 2^logw lanes, one row each; lane l of a group moves EPL
-// elements of column slice blockIdx.y.
-template <typename TI, typename TO, int EPL>
-__global__ void __launch_bounds__(256) lookup_kernel(const TI *__restrict__ T, int K, int D,
-                                                     const int32_t *__restrict__ ids, long long rows, int N, int B,
-                                                     float scale, TO *__restrict__ Y, int logw, int *status) {
-  constexpr int VB = EPL * (int)sizeof(TI);
+// Vectors in flight per lane: the rows' round trip through L2 has to be covered
+// (1 M x 128 fp16 rows of a 1,024-row table: 50 us; with the rows of a step
+// loaded and stored before the next step's are asked for 58 us), with 4 blocks
+// an SM.  Narrow vectors need more of them (50,001 x 1,002 fp32 to bf16, 8-byte
+// loads: 34.5 us with 8, 44 to 47 us with 4) and leave the registers for it.
+template <int EPL> constexpr int kLookDepth = EPL <= 2 ? 8 : 4;
+// Groups of W = 2^logw lanes, one row at a time each; a lane has U vectors of
+// EPL elements in flight: of U rows (W vectors cover a row), or, WIDE, of one
+// row (slice blockIdx.y of its columns; one label and one address serve U
+// vectors).  A warp takes 32 consecutive rows at a time: its lanes hold their
+// labels, the next 32 labels are already on their way, and the rows of one
+// step are loaded before those of the step before are scaled and stored, so
+// that neither the labels' nor the rows' round trip is waited for in full.
+template <typename TI, typename TO, int EPL, bool WIDE>
+__global__ void __launch_bounds__(256, 4) lookup_kernel(const TI *__restrict__ T, int K, int D,
+                                                        const int32_t *__restrict__ ids, int rows, int N, int B,
+                                                        float scale, TO *__restrict__ Y, int logw, int *status) {
+  constexpr int VB = EPL * (int)sizeof(TI), U = kLookDepth<EPL>;
+  using V = typename Raw<VB>::type;
   const int lane = threadIdx.x & 31;
-  const int col = ((blockIdx.y << logw) + (lane & ((1 << logw) - 1))) * EPL;
-  const int per = 32 >> logw;  // rows of a warp's step
-  const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const long long r0 = warp * (kLookRows * per) + (lane >> logw);
-  if (col >= D) return;
-  typename Raw<VB>::type v[kLookRows];
-  bool have[kLookRows], bad = false;
+  const int W = 1 << logw;
+  const int col = ((WIDE ? U : 1) * (int)blockIdx.y * W + (lane & (W - 1))) * EPL;
+  const int per = 32 >> logw, sub = lane >> logw;
+  const int take = WIDE ? per : min(U * per, 32), steps = 32 / take;  // rows of a step, steps of 32 rows
+  const long long stride = (long long)gridDim.x * (8 * 32);
+  const TI *Tc = T + col;
+  TO *Yc = Y + col;
+  bool bad = false;
+  // a label as the row of the B x K table it names, or -1
+  auto row_of = [&](long long r) {
+    if (r >= rows) return -1;
+    const int id = __ldg(ids + r);
+    const bool ok = (unsigned)id < (unsigned)K;
+    bad |= !ok && id != -1;
+    return ok ? (B > 1 ? (int)r / N * K + id : id) : -1;
+  };
+  auto load = [&](V *v, int k32, int j) {
+    if (WIDE) {
+      const int k = __shfl_sync(0xffffffffu, k32, j * take + sub);
+      const TI *p = Tc + (size_t)(unsigned)max(k, 0) * (unsigned)D;
 #pragma unroll
-  for (int u = 0; u < kLookRows; ++u) {
-    const long long r = r0 + u * per;
-    const int id = r < rows ? __ldg(ids + r) : -1;
-    have[u] = (unsigned)id < (unsigned)K;
-    bad |= !have[u] && id != -1;
-    if (have[u]) {
-      const long long b = B > 1 ? r / N : 0;
-      v[u] = ld_raw<VB>(T + (size_t)(b * K + id) * D + col);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kLookRows; ++u) {
-    const long long r = r0 + u * per;
-    if (r >= rows) break;
-    float f[EPL];
-    if (have[u]) {
-      unpack_raw<TI, VB>(v[u], f);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) f[i] *= scale;
+      for (int u = 0; u < U; ++u) {
+        v[u] = V();
+        if (k >= 0 && col + u * W * EPL < D) v[u] = ld_raw<VB>(p + u * W * EPL);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) f[i] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int k = __shfl_sync(0xffffffffu, k32, (j * take + u * per + sub) & 31);
+        v[u] = V();
+        if (k >= 0 && col < D) v[u] = ld_raw<VB>(Tc + (size_t)(unsigned)k * (unsigned)D);
+      }
     }
-    st_vec<TO, EPL>(Y + (size_t)r * D + col, f);
+  };
+  auto put = [&](const V &v, TO *p) {
+    float f[EPL];
+    unpack_raw<TI, VB>(v, f);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) f[i] *= scale;
+    st_vec<TO, EPL>(p, f);
+  };
+  auto store = [&](const V *v, long long r32, int j) {
+    if (WIDE) {
+      const int r = (int)r32 + j * take + sub;  // below 2^31 + 32: compared unsigned
+      if ((unsigned)r < (unsigned)rows) {
+        TO *p = Yc + (size_t)(unsigned)r * (unsigned)D;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (col + u * W * EPL < D) put(v[u], p + u * W * EPL);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = j * take + u * per + sub;
+        if (u * per < take && col < D && r32 + at < rows)
+          put(v[u], Yc + (size_t)(unsigned)((int)r32 + at) * (unsigned)D);
+      }
+    }
+  };
+  long long r32 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 32;
+  if (r32 >= rows) return;
+  int now = row_of(r32 + lane), next = row_of(r32 + stride + lane);
+  V x[U], y[U];
+  load(x, now, 0);
+  int j = 0;
+  auto turn = [&](V *cur, V *nxt) {  // loads the step after this one, stores this one
+    const long long at = r32;
+    const int jj = j;
+    if (++j == steps) {
+      j = 0;
+      r32 += stride;
+      now = next;
+      load(nxt, now, 0);
+      next = row_of(r32 + stride + lane);
+    } else {
+      load(nxt, now, j);
+    }
+    store(cur, at, jj);
+  };
+  while (r32 < rows) {
+    turn(x, y);
+    if (r32 >= rows) break;
+    turn(y, x);
   }
   if (bad) record_status(status, kStBadLabel);
 }
 
 template <typename TI, typename TO, int EPL>
 static void launch_lookup_as(const LookupArgs &a, int *status, cudaStream_t s) {
+  constexpr int U = kLookDepth<EPL>;
   const int vecs = a.D / EPL;
+  // WIDE from two lanes a row on: a lone lane's 16-byte stores would leave
+  // half-written 32-byte sectors behind
+  const bool wide = vecs >= 2 * U;
+  const int each = wide ? (vecs + U - 1) / U : vecs;  // lanes that a row could use
   int logw = 0;
-  while (logw < 5 && (1 << logw) < vecs) ++logw;
-  const int slices = (vecs + (1 << logw) - 1) >> logw;
-  const long long rows = (long long)a.B * a.N, per_block = 8ll * kLookRows * (32 >> logw);
-  lookup_kernel<TI, TO, EPL><<<dim3((unsigned)((rows + per_block - 1) / per_block), slices), 256, 0, s>>>(
-      (const TI *)a.T, a.K, a.D, a.ids, rows, a.N, a.B, a.scale, (TO *)a.Y, logw, status);
+  while (logw < 5 && (1 << logw) < each) ++logw;
+  const int slices = (each + (1 << logw) - 1) >> logw;
+  const long long rows = (long long)a.B * a.N, need = (rows + 255) / 256;
+  const long long wave = (148 * 4 + slices - 1) / slices;
+  const dim3 grid((unsigned)(need < wave ? need : wave), slices);
+  const auto kernel = wide ? lookup_kernel<TI, TO, EPL, true> : lookup_kernel<TI, TO, EPL, false>;
+  kernel<<<grid, 256, 0, s>>>((const TI *)a.T, a.K, a.D, a.ids, (int)rows, a.N, a.B, a.scale, (TO *)a.Y, logw, status);
 }
 template <typename TI, typename TO> static void launch_lookup_to(const LookupArgs &a, int *status, cudaStream_t s) {
   constexpr int widest = 16 / (int)(sizeof(TI) > sizeof(TO) ? sizeof(TI) : sizeof(TO));
