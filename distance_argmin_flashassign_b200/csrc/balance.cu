@@ -26,408 +26,872 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two fp32 operations an instruction: the kernels are bound by issue slots
+// before they are by HBM (a logit costs an unpack, half a maximum, half a
+// product and sum each, and one ex2).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
-// VL consecutive elements of T.
-template <typename T, int VL> struct Pack {
-  T e[VL];
+template <typename T> constexpr bool kIsHalf = std::is_same<T, __half>::value;
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (kIsHalf<T>) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float2 v) {
+  uint32_t w;
+  if constexpr (kIsHalf<T>) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    memcpy(&w, &h, 4);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    memcpy(&w, &h, 4);
+  }
+  return w;
+}
+template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // ignores NaN
+  uint32_t w;
+  if constexpr (kIsHalf<T>) asm("max.f16x2 %0, %1, %2;" : "=r"(w) : "r"(a), "r"(b));
+  else asm("max.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(a), "r"(b));
+  return w;
+}
+
+// The columns a lane holds of one row: P packs of VL consecutive elements
+// (a whole 16 bytes, or a single element), as they lie in memory.  A row of
+// which nothing is looked at, and columns past E, count as -inf.
+template <typename T, int VL, int P> struct Lane {
+  static constexpr int NE = VL * P, NP = (NE + 1) / 2;  // columns, pairs of them
+  static constexpr bool kWords = VL > 1 && sizeof(T) == 2;
+  uint4 w[VL > 1 ? P : 1];
+  float e[VL > 1 ? 1 : P];
+  // p-th pack from column c of `row` in shared memory
+  __device__ __forceinline__ void load(int p, const T *row, int c, bool ok) {
+    if constexpr (VL == 1) {
+      e[p] = ok ? to_f32<T>(row[c]) : neg_inf();
+    } else {
+      const unsigned n = sizeof(T) == 4 ? 0xff800000u : kIsHalf<T> ? 0xfc00fc00u : 0xff80ff80u;
+      w[p] = make_uint4(n, n, n, n);
+      if (ok) w[p] = *reinterpret_cast<const uint4 *>(row + c);
+    }
+  }
+  __device__ __forceinline__ float max() const {
+    float m = neg_inf();
+    if constexpr (kWords) {
+      uint32_t t = w[0].x;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (p > 0) t = max2<T>(t, w[p].x);
+        t = max2<T>(max2<T>(t, w[p].y), max2<T>(w[p].z, w[p].w));
+      }
+      const float2 f = unpack2<T>(t);
+      m = fmaxf(m, fmaxf(f.x, f.y));
+    } else {
+      float2 z[NP];
+      values(z);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) m = fmaxf(m, fmaxf(z[i].x, z[i].y));
+    }
+    return m;
+  }
+  __device__ __forceinline__ void values(float2 *z) const {
+    if constexpr (VL == 1) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) z[i] = make_float2(e[2 * i], 2 * i + 1 < P ? e[2 * i + 1] : neg_inf());
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        z[2 * p] = make_float2(__uint_as_float(w[p].x), __uint_as_float(w[p].y));
+        z[2 * p + 1] = make_float2(__uint_as_float(w[p].z), __uint_as_float(w[p].w));
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        z[4 * p] = unpack2<T>(w[p].x);
+        z[4 * p + 1] = unpack2<T>(w[p].y);
+        z[4 * p + 2] = unpack2<T>(w[p].z);
+        z[4 * p + 3] = unpack2<T>(w[p].w);
+      }
+    }
+  }
+  // stores the p-th pack of z, or zeros, from column c of `row`
+  __device__ __forceinline__ static void store(int p, const float2 *z, bool zero, T *row, int c) {
+    if constexpr (VL == 1) {
+      const float v = p & 1 ? z[p / 2].y : z[p / 2].x;
+      row[c] = from_f32<T>(zero ? 0.f : v);
+    } else {
+      uint4 o;
+      if constexpr (sizeof(T) == 4) {
+        o = make_uint4(__float_as_uint(z[2 * p].x), __float_as_uint(z[2 * p].y), __float_as_uint(z[2 * p + 1].x),
+                       __float_as_uint(z[2 * p + 1].y));
+      } else {
+        o = make_uint4(pack2<T>(z[4 * p]), pack2<T>(z[4 * p + 1]), pack2<T>(z[4 * p + 2]), pack2<T>(z[4 * p + 3]));
+      }
+      if (zero) o = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4 *>(row + c) = o;
+    }
+  }
 };
-template <typename T, int VL> __device__ __forceinline__ void ld_pack(const T *p, float *v) {
-  constexpr int VB = VL * (int)sizeof(T);
-  Pack<T, VL> k;
-  if constexpr (VB == 16) {
-    const uint4 r = *reinterpret_cast<const uint4 *>(p);
-    memcpy(&k, &r, 16);
-  } else {
-    static_assert(VL == 1, "whole 16-byte packs or single elements");
-    k.e[0] = *p;
-  }
-#pragma unroll
-  for (int i = 0; i < VL; ++i) v[i] = to_f32<T>(k.e[i]);
-}
-template <typename T, int VL> __device__ __forceinline__ void st_pack(T *p, const float *v) {
-  constexpr int VB = VL * (int)sizeof(T);
-  Pack<T, VL> k;
-#pragma unroll
-  for (int i = 0; i < VL; ++i) k.e[i] = from_f32<T>(v[i]);
-  if constexpr (VB == 16) {
-    uint4 r;
-    memcpy(&r, &k, 16);
-    *reinterpret_cast<uint4 *>(p) = r;
-  } else {
-    *p = k.e[0];
-  }
-}
 
 constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
-constexpr int kBalLane = 32;  // columns a lane holds at most
+constexpr int kBalLane = 32, kBalSome = 16;  // columns a lane holds at most, and where a warp has lanes to spare
+// Lanes of a team, as a power of two, where the kernel is compiled for them:
+constexpr int kWide = 8;      // the whole block
+constexpr int kAnyTeam = -1;  // up to a warp, known at run time
 
-// Teams: a row belongs to G = 2^logg lanes of a warp, or (WIDE) to the whole
-// block; lane l holds the packs l, l + G, l + 2G, ... of VL columns each.
-struct Team {
-  int logg, lane, row0, rows;  // lane in the team; the block's first row's team; teams a block
-};
-template <bool WIDE> __device__ __forceinline__ Team team_of(int logg) {
-  Team t;
-  if (WIDE) {
-    t.logg = 8;
-    t.lane = threadIdx.x;
-    t.row0 = 0;
-    t.rows = 1;
-  } else {
-    t.logg = logg;
-    t.lane = threadIdx.x & ((1 << logg) - 1);
-    t.row0 = threadIdx.x >> logg;
-    t.rows = kBalThreads >> logg;
+#ifndef BB8
+#define BB8 3
+#define BB16 2
+#define BU8 2
+#define BU16 2
+#endif
+// Blocks that fit an SM next to a lane's columns in registers.
+constexpr int bal_blocks(int NE) { return NE <= 8 ? BB8 : BB16; }
+template <int NE> constexpr int kBalBlocks = bal_blocks(NE);
+// Rows a team works on at a time, so that one row's exchanges between lanes
+// are not waited for alone.
+constexpr int bal_rows(int NE) { return NE <= 8 ? BU8 : NE <= 16 ? BU16 : 1; }
+template <int NE> constexpr int kBalRows = bal_rows(NE);
+
+// Rows go tile by tile to owners: a warp, whose G = 2^logg-lane teams take
+// one row each, or (WIDE) the whole block as one team.  Lane l of a team holds
+// the packs l, l + G, l + 2G, ... of VL columns each.
+template <bool WIDE> struct Owner {
+  int index, count;    // among the owners of the block
+  int lane, row0, rows;  // lane in the team, the team's first row of a step, rows of a step
+  int thread, threads;
+  __device__ __forceinline__ explicit Owner(int logg) {
+    index = WIDE ? 0 : threadIdx.x >> 5;
+    count = WIDE ? 1 : kBalWarps;
+    threads = WIDE ? kBalThreads : 32;
+    thread = threadIdx.x % threads;
+    lane = WIDE ? threadIdx.x : threadIdx.x & ((1 << logg) - 1);
+    row0 = WIDE ? 0 : (threadIdx.x & 31) >> logg;
+    rows = WIDE ? 1 : 32 >> logg;
   }
-  return t;
+  __device__ __forceinline__ void sync() const {
+    if (WIDE) __syncthreads();
+    else __syncwarp();
+  }
+  // sync, and whether any of the owner's threads says so
+  __device__ __forceinline__ bool any(bool v) const {
+    return WIDE ? __syncthreads_or(v) != 0 : __any_sync(0xffffffffu, v) != 0;
+  }
+};
+
+// ------------------------------------------------------------ row tiles ---
+// Rows are consecutive in memory, so a tile of them is one range of bytes of
+// each array.  One thread of an owner copies the ranges of a tile into a stage
+// of shared memory with bulk copies, a few tiles ahead of the owner's work.  A bulk copy
+// moves whole aligned 16-byte pieces: a range is widened to them (its data
+// then starts (address mod 16) bytes into its place), except at the very ends
+// of the array, where what the pieces inside it leave is copied byte by byte.
+struct Span {
+  const char *lo;  // the whole pieces
+  uint32_t bytes;
+};
+// The pieces of [a, a + n), which lies inside the array: with neighbours on
+// both sides every piece that the range touches belongs to the array.
+__device__ __forceinline__ Span span_inside(const char *a, uint32_t n) {
+  const uint32_t skew = (uint32_t)(uintptr_t)a & 15;
+  return {a - skew, (skew + n + 15) & ~15u};
+}
+// The same at the ends of the array [base, base + total): only whole pieces of
+// it, and the bytes of the range that they do not cover copied to dst (the
+// place of a's own piece).
+__device__ __noinline__ Span span_at_ends(const char *a, uint32_t n, const char *base, size_t total, char *dst) {
+  const char *from = (const char *)((uintptr_t)a & ~(uintptr_t)15), *end = a + n;
+  const char *lo = from < base ? from + 16 : from;
+  const char *hi = (const char *)(((uintptr_t)end + 15) & ~(uintptr_t)15);
+  if (hi > base + total) hi -= 16;
+  if (hi < lo) hi = lo;
+  for (const char *q = a; q < end && q < lo; ++q) dst[q - from] = *q;
+  for (const char *q = hi < a ? a : hi; q < end; ++q) dst[q - from] = *q;
+  return {lo, (uint32_t)(hi - lo)};
+}
+__device__ __forceinline__ void bulk_copy(const Span &v, const char *a, char *dst, uint32_t bar) {
+  if (v.bytes == 0) return;
+  const char *from = (const char *)((uintptr_t)a & ~(uintptr_t)15);
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst + (v.lo - from))),
+               "l"(v.lo), "r"(v.bytes), "r"(bar)
+               : "memory");
+}
+// Rows [r, r + n) of up to three arrays of `all` rows of row bytes z, mid and
+// small (a null array is left out) into a stage, completing on `bar`.
+struct Arrays {
+  const char *z, *mid, *small;
+  uint32_t zrow, midrow;  // bytes of a row (small: 1)
+};
+__device__ __forceinline__ void issue_tile(const Arrays &v, size_t r, uint32_t n, size_t all, char *stage, int zplace,
+                                           int midplace, uint32_t bar) {
+  const char *z = v.z + r * v.zrow, *c = v.mid + r * v.midrow, *k = v.small + r;
+  char *zd = stage, *cd = stage + zplace, *kd = cd + midplace;
+  Span sz, sc, sk = {nullptr, 0};
+  // 16 rows hold at least 16 bytes of any of the arrays
+  if (r >= 16 && r + n + 16 <= all) {
+    sz = span_inside(z, n * v.zrow);
+    sc = span_inside(c, n * v.midrow);
+    if (v.small) sk = span_inside(k, n);
+  } else {
+    sz = span_at_ends(z, n * v.zrow, v.z, all * v.zrow, zd);
+    sc = span_at_ends(c, n * v.midrow, v.mid, all * v.midrow, cd);
+    if (v.small) sk = span_at_ends(k, n, v.small, all, kd);
+  }
+  mbar_arrive_expect_tx(bar, sz.bytes + sc.bytes + sk.bytes);
+  bulk_copy(sz, z, zd, bar);
+  bulk_copy(sc, c, cd, bar);
+  if (v.small) bulk_copy(sk, k, kd, bar);
 }
 
-template <typename T, int VL, int P, bool WIDE>
-__global__ void __launch_bounds__(kBalThreads) balance_rows_kernel(const T *__restrict__ Z,
-                                                                   const int32_t *__restrict__ ids,
-                                                                   const uint8_t *__restrict__ mask, int N, int E,
-                                                                   int M, int logg, float *__restrict__ lse,
-                                                                   float *__restrict__ psum, int *__restrict__ csum,
-                                                                   int *__restrict__ tsum, int *status) {
-  constexpr int NE = VL * P;
-  extern __shared__ int smem[];
-  int *hist = smem;                                   // [E] chosen columns of the block's rows
-  float *cols = reinterpret_cast<float *>(smem + E);  // [E] column sums
-  __shared__ float wm[2][kBalWarps], wsum[2][kBalWarps];
-  __shared__ int taken[kBalWarps];
-  const float ninf = __int_as_float(0xff800000);
-  const Team t = team_of<WIDE>(logg);
-  const int b = blockIdx.y, G = 1 << t.logg;
-  const T *Zb = Z + (size_t)b * N * E;
+// Tiles of `rows` rows; the places of a stage in bytes: logits, labels (or
+// lse), mask.
+struct Stage {
+  int rows, z, mid, small;
+  int stages;  // of an owner
+  __host__ __device__ int bytes() const { return z + mid + small; }
+  // the rows' maxima and sums; every place is whole 16-byte pieces
+  __host__ __device__ int stats() const { return (rows * 8 + 15) / 16 * 16; }
+};
+constexpr int kMaxStages = 4;
+// After a wait that ran out at tile q (of every hop-th) in stage `at`: let the
+// copies in flight land, within a second each.
+__device__ __forceinline__ void drain(uint64_t *full, const Stage &st, int q, int hop, int ntiles, int at, int phase) {
+  for (int i = 0; i < st.stages && q + (long long)i * hop < ntiles; ++i) {
+    const bool wrapped = at + i >= st.stages;
+    mbar_wait_for(smem_u32(&full[wrapped ? at + i - st.stages : at + i]), wrapped ? phase ^ 1 : phase, 1000000000ull);
+  }
+}
+
+// Sum over the block of one double a thread, in a fixed order, to thread 0.
+template <int WARPS> __device__ __forceinline__ double block_sum(double v, double *part) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double sum = 0.0;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < WARPS; ++i) sum += part[i];
+  return sum;
+}
+
+struct BalanceOut {
+  float *loss;
+  int32_t *counts, *tokens;
+  float *meanp;
+  float coef;
+};
+// Column e of problem b: its probability sum p and count c of the n rows; returns p / n * c.
+__device__ __forceinline__ double put_column(const BalanceOut &o, int b, int E, int e, double p, int c, int n) {
+  if (n > 0) p /= (double)n;
+  o.counts[(size_t)b * E + e] = c;
+  if (o.meanp) o.meanp[(size_t)b * E + e] = (float)p;
+  return p * (double)c;
+}
+__device__ __forceinline__ void put_loss(const BalanceOut &o, int b, int E, int M, double sum, int n) {
+  o.loss[b] = n > 0 ? (float)((double)o.coef * E * sum / ((double)M * n)) : 0.f;
+  o.tokens[b] = n;
+}
+
+// With one block a problem the block writes the results itself; with more
+// they leave partial rows for balance_join_kernel.
+template <typename T, int VL, int P, int LOGG>
+__global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
+    balance_rows_kernel(const T *__restrict__ Z, const int32_t *__restrict__ ids, const uint8_t *__restrict__ mask,
+                        int B, int N, int E, int M, int logg_, Stage st, float *__restrict__ lse,
+                        float *__restrict__ psum, int *__restrict__ csum, int *__restrict__ tsum, BalanceOut out,
+                        DevCtl ctl) {
+  constexpr bool WIDE = LOGG == kWide;
+  using L = Lane<T, VL, P>;
+  constexpr int NE = L::NE, NP = L::NP, U = kBalRows<NE>;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ __align__(8) uint64_t bars[WIDE ? 1 : kBalWarps][kMaxStages];
+  __shared__ float wm[2][U][kBalWarps], wsum[2][U][kBalWarps];
+  __shared__ int taken[kBalWarps], abort_flag;
+  __shared__ double part[kBalWarps];
+  const int logg = LOGG >= 0 ? LOGG : logg_;
+  const Owner<WIDE> t(logg);
+  const int b = blockIdx.y, G = 1 << logg;
+  uint64_t *full = bars[t.index];
+  // the owner's stages, then its rows' maxima and sums; then the block's columns
+  const int own = st.stages * st.bytes() + st.stats();
+  char *stage = smem + t.index * own;
+  float2 *stat = reinterpret_cast<float2 *>(stage + st.stages * st.bytes());
+  int *hist = reinterpret_cast<int *>(smem + t.count * own);  // [E] chosen columns of the block's rows
+  float *cols = reinterpret_cast<float *>(hist + E);          // [E] column sums
+  const size_t first = (size_t)b * N, all = (size_t)B * N;    // the problem's first row; rows in all
+  const int ntiles = (N + st.rows - 1) / st.rows;
+  const int q0 = blockIdx.x * t.count + t.index, hop = gridDim.x * t.count;  // this owner's tiles
+  if (t.thread == 0)
+    for (int i = 0; i < st.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+  if (threadIdx.x == 0) abort_flag = 0;
+  fence_mbar_init();
   for (int e = threadIdx.x; e < E; e += kBalThreads) {
     hist[e] = 0;
     cols[e] = 0.f;
   }
   __syncthreads();
   wait_prior_grid();
-  float acc[NE];
+
+  auto rows_of = [&](int q) { return min(st.rows, N - q * st.rows); };
+  const Arrays arrays{(const char *)Z, (const char *)ids, (const char *)mask, (uint32_t)(E * sizeof(T)), (uint32_t)M * 4};
+  auto issue = [&](int q, int i) {  // one thread: tile q into stage i
+    issue_tile(arrays, first + (size_t)q * st.rows, rows_of(q), all, stage + i * st.bytes(), st.z, st.mid,
+               smem_u32(&full[i]));
+  };
+  if (t.thread == 0)
+    for (int i = 0; i < st.stages; ++i)
+      if (q0 + (long long)i * hop < ntiles) issue(q0 + i * hop, i);
+
+  float2 acc[NP];
 #pragma unroll
-  for (int i = 0; i < NE; ++i) acc[i] = 0.f;
-  int mytok = 0, buf = 0;
+  for (int i = 0; i < NP; ++i) acc[i] = both(0.f);
+  int mytok = 0, buf = 0, at = 0, phase = 0;
   bool bad = false;
-  for (long long r0 = (long long)blockIdx.x * t.rows; r0 < N; r0 += (long long)gridDim.x * t.rows) {
-    const long long r = r0 + t.row0;
-    const bool live = r < N && (!mask || mask[(size_t)b * N + r] != 0);
-    float z[NE];
+  long long q = q0;
+  for (; q < ntiles; q += hop) {
+    mbar_wait(smem_u32(&full[at]), phase, &abort_flag, ctl);
+    const int n = rows_of((int)q);
+    const size_t r0 = first + (size_t)q * st.rows;
+    const char *d = stage + at * st.bytes();
+    const T *zs = reinterpret_cast<const T *>(d + ((uintptr_t)(Z + r0 * E) & 15));
+    const int *cs = reinterpret_cast<const int *>(d + st.z + ((uintptr_t)(ids + r0 * M) & 15));
+    const uint8_t *ms = reinterpret_cast<const uint8_t *>(d + st.z + st.mid + ((uintptr_t)(mask + r0) & 15));
+    // every team a row: probabilities into the column sums, maximum and sum kept
+    for (int s0 = 0; s0 < n; s0 += U * t.rows) {
+      L x[U];
+      float m[U], s[U], sum[U];
+      float2 z[U][NP];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = (p * G + t.lane) * VL;
-      if (live && c < E) {
-        ld_pack<T, VL>(Zb + (size_t)r * E + c, z + p * VL);
-      } else {
+      for (int u = 0; u < U; ++u) {
+        const int r = s0 + u * t.rows + t.row0;
+        const bool live = r < n && (!mask || ms[r] != 0);
+        const T *row = zs + r * E;
 #pragma unroll
-        for (int i = 0; i < VL; ++i) z[p * VL + i] = ninf;
+        for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, live && (p * G + t.lane) * VL < E);
+        m[u] = x[u].max();
       }
-    }
-    float m = ninf;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) m = fmaxf(m, z[i]);
-    for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // a team without a logit above -inf takes 0 for its maximum: its sum is 0 (or NaN)
-    if (m == ninf) m = 0.f;
-    const float m0 = m;
-    if (fabsf(m) > 1e38f) {  // m log2(e) would overflow (a row of the type's lowest values)
+      for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < NE; ++i) z[i] -= m;
-      m = 0.f;
-    }
-    float s = 0.f;
+        for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      z[i] = exp2_fast(fmaf(z[i], kLog2e, -m * kLog2e));
-      s += z[i];
-    }
-    for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    float factor;  // p_e = z[e] factor
-    float l;
-    if (WIDE) {
-      // z holds exp(z - the warp's maximum): one exchange of the warps' maxima and sums
-      if ((threadIdx.x & 31) == 0) {
-        wm[buf][threadIdx.x >> 5] = s == 0.f ? ninf : m0;
-        wsum[buf][threadIdx.x >> 5] = s;
+      for (int u = 0; u < U; ++u) {
+        // a team without a logit above -inf takes 0 for its maximum: its sum is 0 (or NaN)
+        if (m[u] == neg_inf()) m[u] = 0.f;
+        x[u].values(z[u]);
+        float top = m[u];
+        if (!kIsHalf<T> && fabsf(top) > 1e38f) {  // its product with log2(e) would overflow (the type's lowest values)
+#pragma unroll
+          for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
+          top = 0.f;
+        }
+        float2 ss = both(0.f);
+        const float2 shift = both(-top * kLog2e);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          z[u][i] = fma2(z[u][i], both(kLog2e), shift);
+          z[u][i].x = exp2_fast(z[u][i].x);
+          z[u][i].y = exp2_fast(z[u][i].y);
+          ss = add2(ss, z[u][i]);
+        }
+        s[u] = ss.x + ss.y;
       }
-      __syncthreads();
-      float M_ = ninf, S = 0.f;
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) M_ = fmaxf(M_, wm[buf][w]);
-      if (M_ == ninf) M_ = 0.f;
+      for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) S += wsum[buf][w] * (wsum[buf][w] == 0.f ? 0.f : exp2_fast((wm[buf][w] - M_) * kLog2e));
+        for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+      if (WIDE) {
+        // z holds exp(z - the warp's maximum): one exchange of the warps' maxima and sums
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            wm[buf][u][threadIdx.x >> 5] = s[u] == 0.f ? neg_inf() : m[u];
+            wsum[buf][u][threadIdx.x >> 5] = s[u];
+          }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = s0 + u * t.rows + t.row0;
+        float factor;  // p_e = z_e factor
+        if (WIDE) {
+          float top = neg_inf();
+          sum[u] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kBalWarps; ++w) top = fmaxf(top, wm[buf][u][w]);
+          if (top == neg_inf()) top = 0.f;
+#pragma unroll
+          for (int w = 0; w < kBalWarps; ++w) {
+            const float v = wsum[buf][u][w];
+            sum[u] += v * (v == 0.f ? 0.f : exp2_fast((wm[buf][u][w] - top) * kLog2e));
+          }
+          // NaN in every warp of a NaN row, 0 in every warp of a row left out
+          factor = sum[u] == 0.f ? 0.f : (s[u] == 0.f ? 0.f : exp2_fast((m[u] - top) * kLog2e)) * rcp_fast(sum[u]);
+          m[u] = top;
+        } else {
+          sum[u] = s[u];
+          factor = sum[u] == 0.f ? 0.f : rcp_fast(sum[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) acc[i] = fma2(z[u][i], both(factor), acc[i]);
+        if (t.lane == 0 && r < n) stat[r] = make_float2(m[u], sum[u]);
+      }
       buf ^= 1;
-      factor = (s == 0.f ? 0.f : exp2_fast((m0 - M_) * kLog2e)) / S;  // NaN in every warp of a NaN row
-      l = M_ + logf(S);
-      s = S;
-    } else {
-      factor = 1.f / s;
-      l = m0 + logf(s);
     }
-    const bool on = live && s != 0.f;
-    if (on) {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] = fmaf(z[i], factor, acc[i]);
-      for (int j = t.lane; j < M; j += G) {
-        const int id = ids[((size_t)b * N + r) * M + j];
-        if ((unsigned)id < (unsigned)E) atomicAdd(hist + id, 1);
-        else bad |= id != -1;
-      }
-    }
-    if (t.lane == 0) {
+    t.sync();
+    // every thread a row: what is done once for each
+    for (int r = t.thread; r < n; r += t.threads) {
+      const float2 v = stat[r];
+      const bool on = v.y != 0.f;  // a masked row has no sum either
       mytok += on;
-      if (lse && r < N) lse[(size_t)b * N + r] = on ? l : __int_as_float(0x7f800000);
+      if (lse) lse[r0 + r] = on ? v.x + logf(v.y) : __int_as_float(0x7f800000);
+      if (on)
+        for (int j = 0; j < M; ++j) {
+          const int id = cs[r * M + j];
+          if ((unsigned)id < (unsigned)E) atomicAdd(hist + id, 1);
+          else bad |= id != -1;
+        }
+    }
+    if (t.any(*(volatile int *)&abort_flag)) break;  // the stage has been read
+    if (t.thread == 0 && q + (long long)st.stages * hop < ntiles) issue((int)q + st.stages * hop, at);
+    if (++at == st.stages) {
+      at = 0;
+      phase ^= 1;
     }
   }
-  if (bad) record_status(status, kStBadLabel);
+  if (q < ntiles && t.thread == 0) drain(full, st, (int)q, hop, ntiles, at, phase);  // a wait ran out
+  if (bad) record_status(ctl.status, kStBadLabel);
   // column sums: over the teams of a warp, then over the warps in order
-  if (WIDE) {
+  float sums[2 * NP];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int c = (i / VL * G + t.lane) * VL + i % VL;
-      if (c < E) cols[c] = acc[i];
-    }
-  } else {
+  for (int i = 0; i < NP; ++i) {
+    sums[2 * i] = acc[i].x;
+    sums[2 * i + 1] = acc[i].y;
+  }
+  if (!WIDE)
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      for (int o = G; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    for (int w = 0; w < kBalWarps; ++w) {
-      if ((int)(threadIdx.x >> 5) == w && (threadIdx.x & 31) < G) {
+    for (int o = G; o < 32; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          const int c = (i / VL * G + t.lane) * VL + i % VL;
-          if (c < E) cols[c] += acc[i];
-        }
+      for (int i = 0; i < NE; ++i) sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], o);
+  for (int w = 0; w < (WIDE ? 1 : kBalWarps); ++w) {
+    if (WIDE || ((int)(threadIdx.x >> 5) == w && (threadIdx.x & 31) < G)) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int c = (i / VL * G + t.lane) * VL + i % VL;
+        if (c < E) cols[c] += sums[i];
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
   for (int o = 16; o > 0; o >>= 1) mytok += __shfl_xor_sync(0xffffffffu, mytok, o);
   if ((threadIdx.x & 31) == 0) taken[threadIdx.x >> 5] = mytok;
   __syncthreads();
-  const size_t part = (size_t)b * gridDim.x + blockIdx.x;
+  int ntok = 0;
+#pragma unroll
+  for (int w = 0; w < kBalWarps; ++w) ntok += taken[w];
+  if (gridDim.x == 1) {
+    double mine = 0.0;
+    for (int e = threadIdx.x; e < E; e += kBalThreads) mine += put_column(out, b, E, e, cols[e], hist[e], ntok);
+    const double sum = block_sum<kBalWarps>(mine, part);
+    if (threadIdx.x == 0) put_loss(out, b, E, M, sum, ntok);
+    return;
+  }
+  const size_t row = (size_t)b * gridDim.x + blockIdx.x;
   for (int e = threadIdx.x; e < E; e += kBalThreads) {
-    psum[part * E + e] = cols[e];
-    csum[part * E + e] = hist[e];
+    psum[row * E + e] = cols[e];
+    csum[row * E + e] = hist[e];
   }
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int w = 0; w < kBalWarps; ++w) n += taken[w];
-    tsum[part] = n;
-  }
+  if (threadIdx.x == 0) tsum[row] = ntok;
 }
 
-// One block per problem: adds the blocks' partial rows in order, in fp64.
-__global__ void __launch_bounds__(1024) balance_join_kernel(const float *__restrict__ psum,
-                                                            const int *__restrict__ csum,
-                                                            const int *__restrict__ tsum, int nparts, int E, int M,
-                                                            float coef, float *__restrict__ loss,
-                                                            int32_t *__restrict__ counts,
-                                                            int32_t *__restrict__ tokens, float *__restrict__ meanp) {
-  __shared__ double part[32];
-  __shared__ int ntok;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// Adds the blocks' partial rows in block order, in fp64.  The CTAs of a
+// cluster share a problem's columns and hand their parts of the loss to the
+// first one through its shared memory; in a CTA, groups of threads share a
+// column's partial rows.
+constexpr int kJoinThreads = 512, kJoinCluster = 8;
+__global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const float *__restrict__ psum,
+                                                                    const int *__restrict__ csum,
+                                                                    const int *__restrict__ tsum, int nparts, int E,
+                                                                    int M, BalanceOut out) {
+  __shared__ double part[kJoinThreads / 32], psub[kJoinThreads], shares[kJoinCluster];
+  __shared__ int csub[kJoinThreads], ntok[kJoinThreads / 32];
+  const int b = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5, tid = threadIdx.x;
+  const int ncta = gridDim.x, rank = blockIdx.x;
+  if (ncta > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   wait_prior_grid();
-  if (w == 0) {
-    int n = 0;
-    for (int q = lane; q < nparts; q += 32) n += tsum[(size_t)b * nparts + q];
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) ntok = n;
-  }
+  int n = 0;
+  for (int q = tid; q < nparts; q += kJoinThreads) n += tsum[(size_t)b * nparts + q];
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if (lane == 0) ntok[w] = n;
   __syncthreads();
-  const int n = ntok;
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) n += ntok[i];
+  const int per = (E + ncta - 1) / ncta, e0 = rank * per, e1 = min(E, e0 + per);
+  int tx = 32;  // columns at a time
+  while (tx < per && tx < kJoinThreads) tx *= 2;
+  const int ty = kJoinThreads / tx, g = tid / tx;
   double mine = 0.0;
-  for (int e = threadIdx.x; e < E; e += 1024) {
+  for (int base = e0; base < e1; base += tx) {
+    const int e = base + tid % tx;
     double p = 0.0;
     int c = 0;
-    for (int q = 0; q < nparts; ++q) {
-      p += (double)psum[((size_t)b * nparts + q) * E + e];
-      c += csum[((size_t)b * nparts + q) * E + e];
+    if (e < e1) {
+      const float *ps = psum + (size_t)b * nparts * E + e;
+      const int *cs = csum + (size_t)b * nparts * E + e;
+#pragma unroll 8
+      for (int q = g; q < nparts; q += ty) {
+        p += (double)ps[(size_t)q * E];
+        c += cs[(size_t)q * E];
+      }
     }
-    if (n > 0) p /= (double)n;
-    counts[(size_t)b * E + e] = c;
-    if (meanp) meanp[(size_t)b * E + e] = (float)p;
-    mine += p * (double)c;
+    psub[tid] = p;
+    csub[tid] = c;
+    __syncthreads();
+    if (g == 0 && e < e1) {
+      for (int i = 1; i < ty; ++i) {
+        p += psub[i * tx + tid];
+        c += csub[i * tx + tid];
+      }
+      mine += put_column(out, b, E, e, p, c, n);
+    }
+    __syncthreads();
   }
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) part[w] = mine;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double sum = 0.0;
-    for (int i = 0; i < 32; ++i) sum += part[i];
-    loss[b] = n > 0 ? (float)((double)coef * E * sum / ((double)M * n)) : 0.f;
-    tokens[b] = n;
+  const double sum = block_sum<kJoinThreads / 32>(mine, part);
+  if (ncta == 1) {
+    if (tid == 0) put_loss(out, b, E, M, sum, n);
+    return;
+  }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");  // the first CTA has started
+  if (tid == 0) {
+    uint32_t dst;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(dst) : "r"(smem_u32(&shares[rank])));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dst), "d"(sum) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  if (rank == 0 && tid == 0) {
+    double all = 0.0;
+    for (int i = 0; i < ncta; ++i) all += shares[i];
+    put_loss(out, b, E, M, all, n);
   }
 }
 
-template <typename T, int VL, int P, bool WIDE>
-__global__ void __launch_bounds__(kBalThreads) balance_grad_kernel(const T *Z, const int32_t *__restrict__ counts,
-                                                                   const int32_t *__restrict__ tokens,
-                                                                   const float *__restrict__ lse,
-                                                                   const float *__restrict__ gloss, int N, int E,
-                                                                   int M, float coef, int logg, T *dZ) {
-  constexpr int NE = VL * P;
-  __shared__ float wdot[2][kBalWarps];
-  const Team t = team_of<WIDE>(logg);
-  const int b = blockIdx.y, G = 1 << t.logg;
-  const T *Zb = Z + (size_t)b * N * E;
-  T *dZb = dZ + (size_t)b * N * E;
+template <typename T, int VL, int P, int LOGG>
+__global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
+    balance_grad_kernel(const T *Z, const int32_t *__restrict__ counts, const int32_t *__restrict__ tokens,
+                        const float *__restrict__ lse, const float *__restrict__ gloss, int B, int N, int E, int M,
+                        float coef, int logg_, Stage st, T *dZ, DevCtl ctl) {
+  constexpr bool WIDE = LOGG == kWide;
+  using L = Lane<T, VL, P>;
+  constexpr int NE = L::NE, NP = L::NP, U = kBalRows<NE>;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ __align__(8) uint64_t bars[WIDE ? 1 : kBalWarps][kMaxStages];
+  __shared__ float wdot[2][U][kBalWarps];
+  __shared__ int abort_flag;
+  const float inf = __int_as_float(0x7f800000);
+  const int logg = LOGG >= 0 ? LOGG : logg_;
+  const Owner<WIDE> t(logg);
+  const int b = blockIdx.y, G = 1 << logg;
+  uint64_t *full = bars[t.index];
+  char *stage = smem + t.index * (st.stages * st.bytes());
+  const size_t first = (size_t)b * N, all = (size_t)B * N;
+  const int ntiles = (N + st.rows - 1) / st.rows;
+  const int q0 = blockIdx.x * t.count + t.index, hop = gridDim.x * t.count;
+  if (t.thread == 0)
+    for (int i = 0; i < st.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+  if (threadIdx.x == 0) abort_flag = 0;
+  fence_mbar_init();
+  __syncthreads();
   wait_prior_grid();
-  const int n = tokens[b] > 0 ? tokens[b] : 1;
-  const float k = (gloss ? gloss[b] : 1.f) * (coef * (float)E / (float)n);
-  float f[NE];
+  auto rows_of = [&](int q) { return min(st.rows, N - q * st.rows); };
+  const Arrays arrays{(const char *)Z, (const char *)lse, nullptr, (uint32_t)(E * sizeof(T)), 4};
+  auto issue = [&](int q, int i) {  // one thread: tile q into stage i
+    issue_tile(arrays, first + (size_t)q * st.rows, rows_of(q), all, stage + i * st.bytes(), st.z, st.mid,
+               smem_u32(&full[i]));
+  };
+  if (t.thread == 0)
+    for (int i = 0; i < st.stages; ++i)
+      if (q0 + (long long)i * hop < ntiles) issue(q0 + i * hop, i);
+
+  const int ntok = tokens[b] > 0 ? tokens[b] : 1;
+  const float k = (gloss ? gloss[b] : 1.f) * (coef * (float)E / (float)ntok);
+  float2 kf[NP];  // k f of the lane's columns
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
+  for (int i = 0; i < 2 * NP; ++i) {
     const int c = (i / VL * G + t.lane) * VL + i % VL;
-    f[i] = c < E ? (float)counts[(size_t)b * E + c] / ((float)M * (float)n) : 0.f;
+    const float v = i < NE && c < E ? k * ((float)counts[(size_t)b * E + c] / ((float)M * (float)ntok)) : 0.f;
+    if (i & 1) kf[i / 2].y = v;
+    else kf[i / 2].x = v;
   }
-  int buf = 0;
-  for (long long r0 = (long long)blockIdx.x * t.rows; r0 < N; r0 += (long long)gridDim.x * t.rows) {
-    const long long r = r0 + t.row0;
-    const float l = r < N ? lse[(size_t)b * N + r] : 0.f;
-    const bool on = r < N && l != __int_as_float(0x7f800000);
-    float z[NE], dot = 0.f;
+  int buf = 0, at = 0, phase = 0;
+  long long q = q0;
+  for (; q < ntiles; q += hop) {
+    mbar_wait(smem_u32(&full[at]), phase, &abort_flag, ctl);
+    const int n = rows_of((int)q);
+    const size_t r0 = first + (size_t)q * st.rows;
+    const char *d = stage + at * st.bytes();
+    const T *zs = reinterpret_cast<const T *>(d + ((uintptr_t)(Z + r0 * E) & 15));
+    const float *ls = reinterpret_cast<const float *>(d + st.z + ((uintptr_t)(lse + r0) & 15));
+    for (int s0 = 0; s0 < n; s0 += U * t.rows) {
+      L x[U];
+      float2 z[U][NP];
+      float l[U], dot[U];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = (p * G + t.lane) * VL;
-      if (on && c < E) {
-        ld_pack<T, VL>(Zb + (size_t)r * E + c, z + p * VL);
+      for (int u = 0; u < U; ++u) {
+        const int r = s0 + u * t.rows + t.row0;
+        l[u] = r < n ? ls[r] : inf;
+        const T *row = zs + r * E;
 #pragma unroll
-        for (int i = 0; i < VL; ++i) z[p * VL + i] = exp2_fast((z[p * VL + i] - l) * kLog2e);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VL; ++i) z[p * VL + i] = 0.f;
+        for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, l[u] != inf && (p * G + t.lane) * VL < E);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < NE; ++i) dot = fmaf(f[i], z[i], dot);
-    for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (WIDE) {
-      if ((threadIdx.x & 31) == 0) wdot[buf][threadIdx.x >> 5] = dot;
-      __syncthreads();
-      dot = 0.f;
+      for (int u = 0; u < U; ++u) {
+        x[u].values(z[u]);
+        float top = l[u];
+        if (!kIsHalf<T> && fabsf(top) > 1e38f && top != inf) {  // as in the forward pass
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) dot += wdot[buf][w];
-      buf ^= 1;
-    }
-    if (r < N) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int c = (p * G + t.lane) * VL;
-        if (c < E) {
-          float o[VL];
-#pragma unroll
-          for (int i = 0; i < VL; ++i) o[i] = on ? k * z[p * VL + i] * (f[p * VL + i] - dot) : 0.f;
-          st_pack<T, VL>(dZb + (size_t)r * E + c, o);
+          for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
+          top = 0.f;
         }
+        float2 dd = both(0.f);
+        const float2 shift = both(-top * kLog2e);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          z[u][i] = fma2(z[u][i], both(kLog2e), shift);  // past E -inf: a probability of 0
+          z[u][i].x = exp2_fast(z[u][i].x);
+          z[u][i].y = exp2_fast(z[u][i].y);
+          dd = fma2(kf[i], z[u][i], dd);
+        }
+        dot[u] = dd.x + dd.y;
+      }
+#pragma unroll
+      for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+      if (WIDE) {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+          for (int u = 0; u < U; ++u) wdot[buf][u][threadIdx.x >> 5] = dot[u];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          dot[u] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kBalWarps; ++w) dot[u] += wdot[buf][u][w];
+        }
+        buf ^= 1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = s0 + u * t.rows + t.row0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) z[u][i] = mul2(z[u][i], add2(kf[i], both(-dot[u])));
+        T *row = dZ + (r0 + r) * E;
+        if (r < n)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            if ((p * G + t.lane) * VL < E) L::store(p, z[u], l[u] == inf, row, (p * G + t.lane) * VL);
       }
     }
+    if (t.any(*(volatile int *)&abort_flag)) break;  // the stage has been read
+    if (t.thread == 0 && q + (long long)st.stages * hop < ntiles) issue((int)q + st.stages * hop, at);
+    if (++at == st.stages) {
+      at = 0;
+      phase ^= 1;
+    }
   }
+  if (q < ntiles && t.thread == 0) drain(full, st, (int)q, hop, ntiles, at, phase);  // a wait ran out
 }
 
 // ---------------------------------------------------------------- host ---
 // How a row of E logits is spread: whole 16-byte packs when the rows and the
-// pointers are whole 16-byte pieces, else single elements; the fewest packs a
-// lane with at most 32 lanes, or the whole block where a lane would hold more
-// than kBalLane columns.
+// pointers are whole 16-byte pieces, else single elements; about 16 columns a
+// lane where that needs no more than a warp, up to kBalLane, and from there on
+// the whole block.  Fewer lanes a row exchange less: with 16 columns a lane in
+// place of 8 ...
 struct Spread {
   int VL, P, logg;
   bool wide;
-  int rows;  // rows of a block's step
+  int rows;      // rows of an owner's step
+  int resident;  // blocks an SM
+  int owners;    // of a block
 };
 static Spread spread_of(int E, DType dt, bool aligned) {
   Spread p{};
   const int full = 16 / (int)dtype_size(dt);
   p.VL = aligned && E % full == 0 ? full : 1;
-  const int packs = (E + p.VL - 1) / p.VL, most = kBalLane / p.VL;
-  const int lanes = (packs + most - 1) / most > 32 ? kBalThreads : 32;
-  p.wide = lanes > 32;
-  p.P = 1;
-  while (p.P * lanes < packs) p.P *= 2;
-  while (!p.wide && (p.P << p.logg) < packs) ++p.logg;
+  const int packs = (E + p.VL - 1) / p.VL, most = kBalLane / p.VL, some = kBalSome / p.VL;
+  p.wide = packs > 32 * most;
+  const int lanes = p.wide ? kBalThreads : 32;
+  while (!p.wide && p.logg < 5 && (some << p.logg) < packs) ++p.logg;
   if (p.wide) p.logg = 8;
-  p.rows = kBalThreads >> p.logg;
+  p.P = 1;
+  // packs a lane: powers of two, and multiples of four from eight on
+  while (p.P * (p.wide ? lanes : 1 << p.logg) < packs) p.P += p.P < 8 ? p.P : 4;
+  p.rows = (lanes >> p.logg) * bal_rows(p.VL * p.P);
+  p.resident = bal_blocks(p.VL * p.P);
+  p.owners = kBalThreads / lanes;
   return p;
 }
 
-// Blocks per problem: about 148 x 4 in all while there are rows for them,
-// more where a team would add over 1,024 rows into one fp32 sum.
-static int balance_blocks(int B, int64_t N, const Spread &p) {
-  const int64_t steps = (N + p.rows - 1) / p.rows;
-  int64_t nb = (148 * 4 + B - 1) / B;
+// Tiles and blocks.  mid: bytes of labels (or lse) a row; extra: bytes a block
+// keeps beside its owners' stages.  A block takes its share of an SM's 220 KB
+// of shared memory; an owner's tile is at most a third of its share (three
+// stages), and smaller where the owners of a wave would not all have one, down
+// to a step's rows.
+struct Grid {
+  Stage st;
+  int blocks;  // per problem
+  int smem;
+};
+static Grid grid_of(int B, int64_t N, int E, DType dt, int mid, int extra, const Spread &p) {
+  Grid g{};
+  const int64_t row = (int64_t)E * dtype_size(dt) + mid + 1, wave = 148 * p.resident / B > 0 ? 148 * p.resident / B : 1;
+  const int64_t room = (220 * 1024 / p.resident - extra - 1024) / p.owners;
+  int64_t R = (room / 3 - 3 * 48) / (row + 3), share = (N + wave * p.owners - 1) / (wave * p.owners);
+  if (share < p.rows) share = p.rows;
+  if (R > share) R = share;
+  R = R < p.rows ? R : R / p.rows * p.rows;
+  if (R > 1024) R = 1024;
+  if (R < 1) R = 1;
+  auto place = [](int64_t bytes) { return (int)((bytes + 30 + 15) / 16 * 16); };  // both ends widened
+  g.st.rows = (int)R;
+  g.st.z = place(R * E * dtype_size(dt));
+  g.st.mid = place(R * mid);
+  g.st.small = place(R);
+  const int64_t tiles = (N + R - 1) / R, per_block = (tiles + p.owners - 1) / p.owners;
+  int64_t stages = (room - g.st.stats()) / g.st.bytes();
+  g.st.stages = (int)(stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages);
+  int64_t nb = wave < per_block ? wave : per_block;
+  // no team adds over 1,024 rows into one fp32 sum
+  const int64_t steps = (N + p.rows * p.owners - 1) / (p.rows * p.owners) * bal_rows(p.VL * p.P);
   if (nb * 1024 < steps) nb = (steps + 1023) / 1024;
-  return (int)(nb < steps ? nb : steps);
+  g.blocks = (int)(nb < per_block ? nb : per_block);
+  g.smem = p.owners * (g.st.stages * g.st.bytes() + g.st.stats()) + extra;
+  return g;
 }
 
 static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
-static size_t parts_bytes(int B, int64_t N, int E, const Spread &p) {
-  const size_t parts = (size_t)B * balance_blocks(B, N, p);
+static size_t parts_bytes(int B, int64_t N, int E, DType dt, bool aligned) {
+  // the most labels a row make the smallest tiles and so the most blocks
+  const size_t parts = (size_t)B * grid_of(B, N, E, dt, 4 * kMaxBalanceM, 8 * E, spread_of(E, dt, aligned)).blocks;
   return 2 * al256(parts * E * 4) + al256(parts * 4);
 }
-// Enough for either alignment of Z.
+// Enough for either alignment of Z and any M.
 size_t balance_workspace_bytes(int B, int64_t N, int E, DType dt) {
-  const size_t a = parts_bytes(B, N, E, spread_of(E, dt, true)), u = parts_bytes(B, N, E, spread_of(E, dt, false));
+  const size_t a = parts_bytes(B, N, E, dt, true), u = parts_bytes(B, N, E, dt, false);
   return a > u ? a : u;
 }
 
-// Calls f with the spread's template arguments.
+// Calls f with the spread's template arguments: every spread that spread_of
+// makes is listed.
 template <typename T, typename F> static void with_spread(const Spread &p, F f) {
   constexpr int V = 16 / (int)sizeof(T);
-#define FK_P(vl, n)                                                                              \
-  if (p.VL == vl && p.P == n) {                                                                  \
-    if (p.wide) return f(std::integral_constant<int, vl>(), std::integral_constant<int, n>(), std::true_type()); \
-    return f(std::integral_constant<int, vl>(), std::integral_constant<int, n>(), std::false_type());            \
-  }
-  FK_P(V, 1) FK_P(V, 2) FK_P(V, 4)
-  if constexpr (V == 4) { FK_P(V, 8) }
-  FK_P(1, 1) FK_P(1, 2) FK_P(1, 4) FK_P(1, 8) FK_P(1, 16) FK_P(1, 32)
+#define FK_P(vl, n, lg)                                                                                           \
+  if (p.VL == vl && p.P == n && (lg == kAnyTeam ? !p.wide : p.logg == lg))                                         \
+    return f(std::integral_constant<int, vl>(), std::integral_constant<int, n>(), std::integral_constant<int, lg>());
+  constexpr int H = kBalSome / V;  // packs a lane where a row takes more than one
+  if constexpr (H == 4) { FK_P(V, 1, 0) }
+  FK_P(V, H / 2, 0)
+  FK_P(V, H, 0) FK_P(V, H, 1) FK_P(V, H, 2) FK_P(V, H, 3) FK_P(V, H, 4) FK_P(V, H, 5) FK_P(V, 2 * H, 5)
+  if constexpr (H == 2) { FK_P(V, 1, kWide) }
+  FK_P(V, 2, kWide) FK_P(V, 4, kWide)
+  if constexpr (H == 4) { FK_P(V, 8, kWide) }
+  FK_P(1, 1, 0) FK_P(1, 2, 0) FK_P(1, 4, 0) FK_P(1, 8, 0) FK_P(1, 12, kAnyTeam) FK_P(1, 16, kAnyTeam)
+  FK_P(1, 20, 5) FK_P(1, 24, 5) FK_P(1, 28, 5) FK_P(1, 32, 5)
+  FK_P(1, 8, kWide) FK_P(1, 12, kWide) FK_P(1, 16, kWide) FK_P(1, 20, kWide) FK_P(1, 24, kWide) FK_P(1, 28, kWide)
+  FK_P(1, 32, kWide)
 #undef FK_P
 }
 
-template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void *ws, int *status, cudaStream_t s) {
+template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void *ws, DevCtl ctl, cudaStream_t s) {
   const Spread p = spread_of(a.E, a.dt, (uintptr_t)a.Z % 16 == 0);
-  const int nb = balance_blocks(a.B, a.N, p);
+  const Grid g = grid_of(a.B, a.N, a.E, a.dt, 4 * a.M, 8 * a.E, p);
+  const int nb = g.blocks;
   const size_t parts = (size_t)a.B * nb;
   float *psum = (float *)ws;
   int *csum = (int *)((char *)ws + al256(parts * a.E * 4));
   int *tsum = (int *)((char *)ws + 2 * al256(parts * a.E * 4));
-  const size_t smem = (size_t)a.E * 8;
-  cudaError_t e = cudaSuccess;
-  with_spread<T>(p, [&](auto vl, auto np, auto wide) {
-    const auto kernel = balance_rows_kernel<T, decltype(vl)::value, decltype(np)::value, decltype(wide)::value>;
-    if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const BalanceOut out{a.loss, a.counts, a.tokens, a.meanp, a.coef};
+  cudaError_t e = cudaErrorNotSupported;
+  with_spread<T>(p, [&](auto vl, auto np, auto lg) {
+    const auto kernel = balance_rows_kernel<T, decltype(vl)::value, decltype(np)::value, decltype(lg)::value>;
+    e = g.smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem) : cudaSuccess;
     if (e == cudaSuccess)
-      e = launch_chained(kernel, dim3(nb, a.B), dim3(kBalThreads), smem, s, (const T *)a.Z, a.ids, a.mask, a.N, a.E, a.M,
-                         p.logg, a.lse, psum, csum, tsum, status);
+      e = launch_chained(kernel, dim3(nb, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.ids, a.mask, a.B, a.N, a.E,
+                         a.M, p.logg, g.st, a.lse, psum, csum, tsum, out, ctl);
   });
-  if (e != cudaSuccess) return e;
-  return launch_chained(balance_join_kernel, dim3(a.B), dim3(1024), 0, s, psum, csum, tsum, nb, a.E, a.M, a.coef, a.loss,
-                        a.counts, a.tokens, a.meanp);
+  count_launches(1);
+  if (e != cudaSuccess || nb == 1) return e;
+  const int ncta = a.E <= 32 ? 1 : a.E >= 32 * kJoinCluster ? kJoinCluster : (a.E + 31) / 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ncta, a.B);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ncta;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, balance_join_kernel, (const float *)psum, (const int *)csum, (const int *)tsum, nb, a.E,
+                            a.M, out);
 }
-cudaError_t launch_balance(const BalanceArgs &a, void *ws, int *status, cudaStream_t s) {
-  count_launches(2);
-  return a.dt == kF32   ? balance_from<float>(a, ws, status, s)
-         : a.dt == kF16 ? balance_from<__half>(a, ws, status, s)
-                        : balance_from<__nv_bfloat16>(a, ws, status, s);
+cudaError_t launch_balance(const BalanceArgs &a, void *ws, DevCtl ctl, cudaStream_t s) {
+  return a.dt == kF32   ? balance_from<float>(a, ws, ctl, s)
+         : a.dt == kF16 ? balance_from<__half>(a, ws, ctl, s)
+                        : balance_from<__nv_bfloat16>(a, ws, ctl, s);
 }
 
-template <typename T> static cudaError_t balance_grad_from(const BalanceGradArgs &a, cudaStream_t s) {
+template <typename T> static cudaError_t balance_grad_from(const BalanceGradArgs &a, DevCtl ctl, cudaStream_t s) {
   const Spread p = spread_of(a.E, a.dt, (uintptr_t)a.Z % 16 == 0 && (uintptr_t)a.dZ % 16 == 0);
-  cudaError_t e = cudaSuccess;
-  with_spread<T>(p, [&](auto vl, auto np, auto wide) {
-    e = launch_chained(balance_grad_kernel<T, decltype(vl)::value, decltype(np)::value, decltype(wide)::value>,
-                       dim3(balance_blocks(a.B, a.N, p), a.B), dim3(kBalThreads), 0, s, (const T *)a.Z, a.counts,
-                       a.tokens, a.lse, a.gloss, a.N, a.E, a.M, a.coef, p.logg, (T *)a.dZ);
+  const Grid g = grid_of(a.B, a.N, a.E, a.dt, 4, 0, p);
+  cudaError_t e = cudaErrorNotSupported;
+  with_spread<T>(p, [&](auto vl, auto np, auto lg) {
+    const auto kernel = balance_grad_kernel<T, decltype(vl)::value, decltype(np)::value, decltype(lg)::value>;
+    e = g.smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem) : cudaSuccess;
+    if (e == cudaSuccess)
+      e = launch_chained(kernel, dim3(g.blocks, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.counts, a.tokens,
+                         a.lse, a.gloss, a.B, a.N, a.E, a.M, a.coef, p.logg, g.st, (T *)a.dZ, ctl);
   });
   return e;
 }
-cudaError_t launch_balance_grad(const BalanceGradArgs &a, cudaStream_t s) {
+cudaError_t launch_balance_grad(const BalanceGradArgs &a, DevCtl ctl, cudaStream_t s) {
   count_launches(1);
-  return a.dt == kF32   ? balance_grad_from<float>(a, s)
-         : a.dt == kF16 ? balance_grad_from<__half>(a, s)
-                        : balance_grad_from<__nv_bfloat16>(a, s);
+  return a.dt == kF32   ? balance_grad_from<float>(a, ctl, s)
+         : a.dt == kF16 ? balance_grad_from<__half>(a, ctl, s)
+                        : balance_grad_from<__nv_bfloat16>(a, ctl, s);
 }
 
 }  // namespace fk

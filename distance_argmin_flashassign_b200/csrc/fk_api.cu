@@ -905,7 +905,7 @@ int64_t fk_balance_workspace(int B, int64_t N, int E, fk_dtype dt) try {
 static fk_status check_balance(int B, int64_t N, int E, fk_dtype dt, int M, float coef) {
   const fk_status st = check_book(B, N, E, "E", kMaxBalanceE, 1, dt);
   if (st != FK_OK) return st;
-  if (M < 1 || M > 64) return fail(FK_ERR_INVALID_ARG, "M must be in [1, 64]");
+  if (M < 1 || M > kMaxBalanceM) return fail(FK_ERR_INVALID_ARG, "M must be in [1, 64]");
   if ((long long)B * N * M >= (1ll << 31)) return fail(FK_ERR_INVALID_ARG, "B*N*M must be < 2^31");
   if (!finite_f(coef)) return fail(FK_ERR_INVALID_ARG, "coef must be finite");
   return FK_OK;
@@ -932,7 +932,7 @@ fk_status fk_balance(const void *Z, int B, int64_t N, int E, fk_dtype dt, const 
   void *work = nullptr;
   if ((st = book_scratch(*d, s, balance_workspace_bytes(B, N, E, (DType)dt), ws, ws_bytes, &work)) != FK_OK) return st;
   const BalanceArgs a{Z, ids, mask, B, (int)N, E, M, (DType)dt, coef, loss, counts, tokens, meanp, lse};
-  const cudaError_t e = launch_balance(a, work, d->status, s);
+  const cudaError_t e = launch_balance(a, work, ctl_of(*d), s);
   return e == cudaSuccess ? FK_OK : cuda_fail(e, "balance kernels");
 } catch (...) {
   return thrown();
@@ -950,7 +950,7 @@ fk_status fk_balance_grad(const void *Z, int B, int64_t N, int E, fk_dtype dt, c
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = device_state_captured(s, &d)) != FK_OK) return st;
   const BalanceGradArgs a{Z, counts, tokens, lse, gloss, B, (int)N, E, M, (DType)dt, coef, dZ};
-  const cudaError_t e = launch_balance_grad(a, s);
+  const cudaError_t e = launch_balance_grad(a, ctl_of(*d), s);
   return e == cudaSuccess ? FK_OK : cuda_fail(e, "balance gradient kernel");
 } catch (...) {
   return thrown();

@@ -155,7 +155,7 @@ size_t lookup_grad_workspace_bytes(int64_t rows, int64_t Ktot, int B, int D, DTy
 cudaError_t launch_lookup_grad(const LookupGradArgs &a, void *ws, int *status, cudaStream_t s);
 
 // ---- balance.cu: balance loss of routed rows --------------------------------
-constexpr int kMaxBalanceE = 8192;  // largest E
+constexpr int kMaxBalanceE = 8192, kMaxBalanceM = 64;  // largest E and M
 struct BalanceArgs {
   const void *Z;        // B x N rows of E logits of dt
   const int32_t *ids;   // B x N x M chosen columns, -1: none
@@ -170,7 +170,7 @@ struct BalanceArgs {
   float *lse;       // B x N or null
 };
 size_t balance_workspace_bytes(int B, int64_t N, int E, DType dt);
-cudaError_t launch_balance(const BalanceArgs &a, void *ws, int *status, cudaStream_t s);
+cudaError_t launch_balance(const BalanceArgs &a, void *ws, DevCtl ctl, cudaStream_t s);
 struct BalanceGradArgs {
   const void *Z;
   const int32_t *counts, *tokens;
@@ -180,7 +180,7 @@ struct BalanceGradArgs {
   float coef;
   void *dZ;
 };
-cudaError_t launch_balance_grad(const BalanceGradArgs &a, cudaStream_t s);
+cudaError_t launch_balance_grad(const BalanceGradArgs &a, DevCtl ctl, cudaStream_t s);
 
 // ---- update.cu: sort-inverse update ---------------------------------------
 enum UpdateMode : int { kMean = 0, kAccumulate = 1 };
