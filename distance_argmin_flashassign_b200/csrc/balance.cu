@@ -244,50 +244,103 @@ __device__ __forceinline__ void bulk_copy(const Span &v, const char *a, char *ds
                "l"(v.lo), "r"(v.bytes), "r"(bar)
                : "memory");
 }
-// Rows [r, r + n) of up to three arrays of `all` rows of row bytes z, mid and
-// small (a null array is left out) into a stage, completing on `bar`.
-struct Arrays {
-  const char *z, *mid, *small;
-  uint32_t zrow, midrow;  // bytes of a row (small: 1)
-};
-__device__ __forceinline__ void issue_tile(const Arrays &v, size_t r, uint32_t n, size_t all, char *stage, int zplace,
-                                           int midplace, uint32_t bar) {
-  const char *z = v.z + r * v.zrow, *c = v.mid + r * v.midrow, *k = v.small + r;
-  char *zd = stage, *cd = stage + zplace, *kd = cd + midplace;
-  Span sz, sc, sk = {nullptr, 0};
-  // 16 rows hold at least 16 bytes of any of the arrays
-  if (r >= 16 && r + n + 16 <= all) {
-    sz = span_inside(z, n * v.zrow);
-    sc = span_inside(c, n * v.midrow);
-    if (v.small) sk = span_inside(k, n);
-  } else {
-    sz = span_at_ends(z, n * v.zrow, v.z, all * v.zrow, zd);
-    sc = span_at_ends(c, n * v.midrow, v.mid, all * v.midrow, cd);
-    if (v.small) sk = span_at_ends(k, n, v.small, all, kd);
-  }
-  mbar_arrive_expect_tx(bar, sz.bytes + sc.bytes + sk.bytes);
-  bulk_copy(sz, z, zd, bar);
-  bulk_copy(sc, c, cd, bar);
-  if (v.small) bulk_copy(sk, k, kd, bar);
+// Rows [r, r + n) of an array of `all` rows of `width` bytes into `dst`; the
+// bytes of whole pieces are returned, to be expected by the barrier, and are
+// copied by bulk_copy.
+__device__ __forceinline__ Span span_of(const char *base, uint32_t width, size_t r, uint32_t n, size_t all, char *dst) {
+  const char *a = base + r * width;
+  // 16 rows hold at least 16 bytes
+  if (r >= 16 && r + n + 16 <= all) return span_inside(a, n * width);
+  return span_at_ends(a, n * width, base, all * width, dst);
 }
 
-// Tiles of `rows` rows; the places of a stage in bytes: logits, labels (or
-// lse), mask.
-struct Stage {
-  int rows, z, mid, small;
-  int stages;  // of an owner
-  __host__ __device__ int bytes() const { return z + mid + small; }
-  // the rows' maxima and sums; every place is whole 16-byte pieces
-  __host__ __device__ int stats() const { return (rows * 8 + 15) / 16 * 16; }
+// An owner has a run of consecutive rows.  Their logits pass through a ring of
+// `stages` tiles of `rows` rows; what is small a row (labels or lse, mask)
+// comes in batches of `batch` rows, whole tiles of at least 32 rows where the
+// owner has them, in two places in turn, so that what is done once a row has a
+// thread for each.  Places in bytes, whole 16-byte pieces.
+struct Plan {
+  int share;               // rows of an owner
+  int rows, stages, z;     // of a tile; tiles; bytes of a tile's place
+  int batch, mid, small;   // rows of a batch; bytes of its places
+  __host__ __device__ int stats() const { return (batch * 8 + 15) / 16 * 16; }  // the rows' maxima and sums
+  __host__ __device__ int bytes() const { return stages * z + 2 * (mid + small) + stats(); }
 };
 constexpr int kMaxStages = 4;
-// After a wait that ran out at tile q (of every hop-th) in stage `at`: let the
-// copies in flight land, within a second each.
-__device__ __forceinline__ void drain(uint64_t *full, const Stage &st, int q, int hop, int ntiles, int at, int phase) {
-  for (int i = 0; i < st.stages && q + (long long)i * hop < ntiles; ++i) {
-    const bool wrapped = at + i >= st.stages;
-    mbar_wait_for(smem_u32(&full[wrapped ? at + i - st.stages : at + i]), wrapped ? phase ^ 1 : phase, 1000000000ull);
+struct Bars {
+  uint64_t tile[kMaxStages], side[2];
+};
+template <bool WIDE> struct Rows {
+  const char *Z, *mid, *small;
+  uint32_t zrow, midrow;  // bytes of a row (small: 1)
+  size_t all;             // rows of the arrays
+  size_t first;           // the owner's first row in them
+  int n, ntiles, nbatches;
+  char *place;
+  Bars *bar;
+  Plan pl;
+  __device__ __forceinline__ char *tile_at(int s) const { return place + s * pl.z; }
+  __device__ __forceinline__ char *mid_at(int s) const { return place + pl.stages * pl.z + s * (pl.mid + pl.small); }
+  __device__ __forceinline__ char *small_at(int s) const { return mid_at(s) + pl.mid; }
+  __device__ __forceinline__ float2 *stats() const { return reinterpret_cast<float2 *>(mid_at(2)); }
+  // where the data of a row lies in its array's place, from the row's own address
+  __device__ __forceinline__ static uint32_t skew(const char *base, uint32_t width, size_t r) {
+    return ((uint32_t)(uintptr_t)base + (uint32_t)r * width) & 15;
   }
+  __device__ __forceinline__ int tile_rows(int k) const { return min(pl.rows, n - k * pl.rows); }
+  __device__ __forceinline__ int batch_rows(int k) const { return min(pl.batch, n - k * pl.batch); }
+  // one thread: tile k into ring place s; batch k into place s
+  __device__ __forceinline__ void issue_tile(int k, int s) const {
+    const size_t r = first + (size_t)(k * pl.rows);
+    const uint32_t b = smem_u32(&bar->tile[s]);
+    const Span v = span_of(Z, zrow, r, tile_rows(k), all, tile_at(s));
+    mbar_arrive_expect_tx(b, v.bytes);
+    bulk_copy(v, Z + r * zrow, tile_at(s), b);
+  }
+  __device__ __forceinline__ void issue_batch(int k, int s) const {
+    const size_t r = first + (size_t)(k * pl.batch);
+    const uint32_t b = smem_u32(&bar->side[s]), c = batch_rows(k);
+    const Span v = span_of(mid, midrow, r, c, all, mid_at(s));
+    Span m = {nullptr, 0};
+    if (small) m = span_of(small, 1, r, c, all, small_at(s));
+    mbar_arrive_expect_tx(b, v.bytes + m.bytes);
+    bulk_copy(v, mid + r * midrow, mid_at(s), b);
+    if (small) bulk_copy(m, small + r, small_at(s), b);
+  }
+  __device__ __forceinline__ void start() const {
+    for (int i = 0; i < 2 && i < nbatches; ++i) issue_batch(i, i);
+    for (int i = 0; i < pl.stages && i < ntiles; ++i) issue_tile(i, i);
+  }
+  // After a wait that ran out at batch kb, tile kt: let the copies in flight
+  // land, within a second each.
+  __device__ __forceinline__ void drain(int kb, int kt) const {
+    for (int i = kb; i < kb + 2 && i < nbatches; ++i) mbar_wait_for(smem_u32(&bar->side[i & 1]), i >> 1 & 1, 1000000000ull);
+    for (int i = kt; i < kt + pl.stages && i < ntiles; ++i)
+      mbar_wait_for(smem_u32(&bar->tile[i % pl.stages]), i / pl.stages & 1, 1000000000ull);
+  }
+};
+
+// The calling thread's owner: its rows of problem b and its places, with the
+// barriers set up (visible after the block's next barrier).
+template <bool WIDE>
+__device__ __forceinline__ Rows<WIDE> owned(const Owner<WIDE> &t, const Plan &pl, Bars *bar, char *smem, int b, int B,
+                                            int N) {
+  Rows<WIDE> v;
+  const long long from = ((long long)blockIdx.x * t.count + t.index) * pl.share;
+  v.n = from < N ? (int)min((long long)pl.share, N - from) : 0;
+  v.first = (size_t)b * N + from;
+  v.all = (size_t)B * N;
+  v.ntiles = (v.n + pl.rows - 1) / pl.rows;
+  v.nbatches = (v.n + pl.batch - 1) / pl.batch;
+  v.place = smem + t.index * pl.bytes();
+  v.bar = bar;
+  v.pl = pl;
+  if (t.thread == 0) {
+    for (int i = 0; i < pl.stages; ++i) mbar_init(smem_u32(&bar->tile[i]), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bar->side[i]), 1);
+    fence_mbar_init();
+  }
+  return v;
 }
 
 // Sum over the block of one double a thread, in a fixed order, to thread 0.
@@ -324,65 +377,53 @@ __device__ __forceinline__ void put_loss(const BalanceOut &o, int b, int E, int 
 template <typename T, int VL, int P, int LOGG>
 __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     balance_rows_kernel(const T *__restrict__ Z, const int32_t *__restrict__ ids, const uint8_t *__restrict__ mask,
-                        int B, int N, int E, int M, int logg_, Stage st, float *__restrict__ lse,
+                        int B, int N, int E, int M, int logg_, Plan pl, float *__restrict__ lse,
                         float *__restrict__ psum, int *__restrict__ csum, int *__restrict__ tsum, BalanceOut out,
                         DevCtl ctl) {
   constexpr bool WIDE = LOGG == kWide;
   using L = Lane<T, VL, P>;
   constexpr int NE = L::NE, NP = L::NP, U = kBalRows<NE>;
   extern __shared__ __align__(128) char smem[];
-  __shared__ __align__(8) uint64_t bars[WIDE ? 1 : kBalWarps][kMaxStages];
+  __shared__ __align__(8) Bars bars[WIDE ? 1 : kBalWarps];
   __shared__ float wm[2][U][kBalWarps], wsum[2][U][kBalWarps];
   __shared__ int taken[kBalWarps], abort_flag;
   __shared__ double part[kBalWarps];
   const int logg = LOGG >= 0 ? LOGG : logg_;
   const Owner<WIDE> t(logg);
   const int b = blockIdx.y, G = 1 << logg;
-  uint64_t *full = bars[t.index];
-  // the owner's stages, then its rows' maxima and sums; then the block's columns
-  const int own = st.stages * st.bytes() + st.stats();
-  char *stage = smem + t.index * own;
-  float2 *stat = reinterpret_cast<float2 *>(stage + st.stages * st.bytes());
-  int *hist = reinterpret_cast<int *>(smem + t.count * own);  // [E] chosen columns of the block's rows
-  float *cols = reinterpret_cast<float *>(hist + E);          // [E] column sums
-  const size_t first = (size_t)b * N, all = (size_t)B * N;    // the problem's first row; rows in all
-  const int ntiles = (N + st.rows - 1) / st.rows;
-  const int q0 = blockIdx.x * t.count + t.index, hop = gridDim.x * t.count;  // this owner's tiles
-  if (t.thread == 0)
-    for (int i = 0; i < st.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+  // the chosen columns of the block's rows [E], then the owners' places, where
+  // the block's column sums [E] lie once the rows are done
+  int *hist = reinterpret_cast<int *>(smem);
+  char *places = smem + (E * 4 + 15) / 16 * 16;
+  float *cols = reinterpret_cast<float *>(places);
+  Rows<WIDE> v = owned<WIDE>(t, pl, &bars[t.index], places, b, B, N);
+  v.Z = (const char *)Z;
+  v.mid = (const char *)ids;
+  v.small = (const char *)mask;
+  v.zrow = (uint32_t)(E * sizeof(T));
+  v.midrow = (uint32_t)M * 4;
   if (threadIdx.x == 0) abort_flag = 0;
-  fence_mbar_init();
-  for (int e = threadIdx.x; e < E; e += kBalThreads) {
-    hist[e] = 0;
-    cols[e] = 0.f;
-  }
+  for (int e = threadIdx.x; e < E; e += kBalThreads) hist[e] = 0;
   __syncthreads();
   wait_prior_grid();
-
-  auto rows_of = [&](int q) { return min(st.rows, N - q * st.rows); };
-  const Arrays arrays{(const char *)Z, (const char *)ids, (const char *)mask, (uint32_t)(E * sizeof(T)), (uint32_t)M * 4};
-  auto issue = [&](int q, int i) {  // one thread: tile q into stage i
-    issue_tile(arrays, first + (size_t)q * st.rows, rows_of(q), all, stage + i * st.bytes(), st.z, st.mid,
-               smem_u32(&full[i]));
-  };
-  if (t.thread == 0)
-    for (int i = 0; i < st.stages; ++i)
-      if (q0 + (long long)i * hop < ntiles) issue(q0 + i * hop, i);
+  if (t.thread == 0) v.start();
 
   float2 acc[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) acc[i] = both(0.f);
-  int mytok = 0, buf = 0, at = 0, phase = 0;
-  bool bad = false;
-  long long q = q0;
-  for (; q < ntiles; q += hop) {
-    mbar_wait(smem_u32(&full[at]), phase, &abort_flag, ctl);
-    const int n = rows_of((int)q);
-    const size_t r0 = first + (size_t)q * st.rows;
-    const char *d = stage + at * st.bytes();
-    const T *zs = reinterpret_cast<const T *>(d + ((uintptr_t)(Z + r0 * E) & 15));
-    const int *cs = reinterpret_cast<const int *>(d + st.z + ((uintptr_t)(ids + r0 * M) & 15));
-    const uint8_t *ms = reinterpret_cast<const uint8_t *>(d + st.z + st.mid + ((uintptr_t)(mask + r0) & 15));
+  int mytok = 0, buf = 0, at = 0, phase = 0, kt = 0, kb = 0;
+  bool bad = false, gave_up = false;
+  float2 *stat = v.stats();
+  for (; kb < v.nbatches && !gave_up; ++kb) {
+    mbar_wait(smem_u32(&v.bar->side[kb & 1]), kb >> 1 & 1, &abort_flag, ctl);
+    const size_t rb = v.first + (size_t)kb * pl.batch;  // the batch's first row
+    const int nrows = v.batch_rows(kb);
+    const int *cs = reinterpret_cast<const int *>(v.mid_at(kb & 1) + v.skew(v.mid, v.midrow, rb));
+    const uint8_t *ms = reinterpret_cast<const uint8_t *>(v.small_at(kb & 1) + v.skew(v.small, 1, rb));
+    for (int in_batch = 0; in_batch < nrows; in_batch += pl.rows, ++kt) {
+    mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
+    const int n = v.tile_rows(kt);
+    const T *zs = reinterpret_cast<const T *>(v.tile_at(at) + v.skew(v.Z, v.zrow, v.first + (size_t)(kt * pl.rows)));
     // every team a row: probabilities into the column sums, maximum and sum kept
     for (int s0 = 0; s0 < n; s0 += U * t.rows) {
       L x[U];
@@ -391,7 +432,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = s0 + u * t.rows + t.row0;
-        const bool live = r < n && (!mask || ms[r] != 0);
+        const bool live = r < n && (!mask || ms[in_batch + r] != 0);
         const T *row = zs + r * E;
 #pragma unroll
         for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, live && (p * G + t.lane) * VL < E);
@@ -461,17 +502,25 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) acc[i] = fma2(z[u][i], both(factor), acc[i]);
-        if (t.lane == 0 && r < n) stat[r] = make_float2(m[u], sum[u]);
+        if (t.lane == 0 && r < n) stat[in_batch + r] = make_float2(m[u], sum[u]);
       }
       buf ^= 1;
     }
-    t.sync();
+    gave_up = t.any(*(volatile int *)&abort_flag);  // the tile has been read
+    if (gave_up) break;
+    if (t.thread == 0 && kt + pl.stages < v.ntiles) v.issue_tile(kt + pl.stages, at);
+    if (++at == pl.stages) {
+      at = 0;
+      phase ^= 1;
+    }
+    }
+    if (gave_up) break;
     // every thread a row: what is done once for each
-    for (int r = t.thread; r < n; r += t.threads) {
-      const float2 v = stat[r];
-      const bool on = v.y != 0.f;  // a masked row has no sum either
+    for (int r = t.thread; r < nrows; r += t.threads) {
+      const float2 w = stat[r];
+      const bool on = w.y != 0.f;  // a masked row has no sum either
       mytok += on;
-      if (lse) lse[r0 + r] = on ? v.x + logf(v.y) : __int_as_float(0x7f800000);
+      if (lse) lse[rb + r] = on ? w.x + logf(w.y) : __int_as_float(0x7f800000);
       if (on)
         for (int j = 0; j < M; ++j) {
           const int id = cs[r * M + j];
@@ -479,16 +528,15 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
           else bad |= id != -1;
         }
     }
-    if (t.any(*(volatile int *)&abort_flag)) break;  // the stage has been read
-    if (t.thread == 0 && q + (long long)st.stages * hop < ntiles) issue((int)q + st.stages * hop, at);
-    if (++at == st.stages) {
-      at = 0;
-      phase ^= 1;
-    }
+    t.sync();  // the batch has been read
+    if (t.thread == 0 && kb + 2 < v.nbatches) v.issue_batch(kb + 2, kb & 1);
   }
-  if (q < ntiles && t.thread == 0) drain(full, st, (int)q, hop, ntiles, at, phase);  // a wait ran out
+  if (gave_up && t.thread == 0) v.drain(kb, kt);
   if (bad) record_status(ctl.status, kStBadLabel);
   // column sums: over the teams of a warp, then over the warps in order
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kBalThreads) cols[e] = 0.f;
+  __syncthreads();
   float sums[2 * NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
@@ -607,38 +655,28 @@ template <typename T, int VL, int P, int LOGG>
 __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     balance_grad_kernel(const T *Z, const int32_t *__restrict__ counts, const int32_t *__restrict__ tokens,
                         const float *__restrict__ lse, const float *__restrict__ gloss, int B, int N, int E, int M,
-                        float coef, int logg_, Stage st, T *dZ, DevCtl ctl) {
+                        float coef, int logg_, Plan pl, T *dZ, DevCtl ctl) {
   constexpr bool WIDE = LOGG == kWide;
   using L = Lane<T, VL, P>;
   constexpr int NE = L::NE, NP = L::NP, U = kBalRows<NE>;
   extern __shared__ __align__(128) char smem[];
-  __shared__ __align__(8) uint64_t bars[WIDE ? 1 : kBalWarps][kMaxStages];
+  __shared__ __align__(8) Bars bars[WIDE ? 1 : kBalWarps];
   __shared__ float wdot[2][U][kBalWarps];
   __shared__ int abort_flag;
   const float inf = __int_as_float(0x7f800000);
   const int logg = LOGG >= 0 ? LOGG : logg_;
   const Owner<WIDE> t(logg);
   const int b = blockIdx.y, G = 1 << logg;
-  uint64_t *full = bars[t.index];
-  char *stage = smem + t.index * (st.stages * st.bytes());
-  const size_t first = (size_t)b * N, all = (size_t)B * N;
-  const int ntiles = (N + st.rows - 1) / st.rows;
-  const int q0 = blockIdx.x * t.count + t.index, hop = gridDim.x * t.count;
-  if (t.thread == 0)
-    for (int i = 0; i < st.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+  Rows<WIDE> v = owned<WIDE>(t, pl, &bars[t.index], smem, b, B, N);
+  v.Z = (const char *)Z;
+  v.mid = (const char *)lse;
+  v.small = nullptr;
+  v.zrow = (uint32_t)(E * sizeof(T));
+  v.midrow = 4;
   if (threadIdx.x == 0) abort_flag = 0;
-  fence_mbar_init();
   __syncthreads();
   wait_prior_grid();
-  auto rows_of = [&](int q) { return min(st.rows, N - q * st.rows); };
-  const Arrays arrays{(const char *)Z, (const char *)lse, nullptr, (uint32_t)(E * sizeof(T)), 4};
-  auto issue = [&](int q, int i) {  // one thread: tile q into stage i
-    issue_tile(arrays, first + (size_t)q * st.rows, rows_of(q), all, stage + i * st.bytes(), st.z, st.mid,
-               smem_u32(&full[i]));
-  };
-  if (t.thread == 0)
-    for (int i = 0; i < st.stages; ++i)
-      if (q0 + (long long)i * hop < ntiles) issue(q0 + i * hop, i);
+  if (t.thread == 0) v.start();
 
   const int ntok = tokens[b] > 0 ? tokens[b] : 1;
   const float k = (gloss ? gloss[b] : 1.f) * (coef * (float)E / (float)ntok);
@@ -650,15 +688,18 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     if (i & 1) kf[i / 2].y = v;
     else kf[i / 2].x = v;
   }
-  int buf = 0, at = 0, phase = 0;
-  long long q = q0;
-  for (; q < ntiles; q += hop) {
-    mbar_wait(smem_u32(&full[at]), phase, &abort_flag, ctl);
-    const int n = rows_of((int)q);
-    const size_t r0 = first + (size_t)q * st.rows;
-    const char *d = stage + at * st.bytes();
-    const T *zs = reinterpret_cast<const T *>(d + ((uintptr_t)(Z + r0 * E) & 15));
-    const float *ls = reinterpret_cast<const float *>(d + st.z + ((uintptr_t)(lse + r0) & 15));
+  int buf = 0, at = 0, phase = 0, kt = 0, kb = 0;
+  bool gave_up = false;
+  for (; kb < v.nbatches && !gave_up; ++kb) {
+    mbar_wait(smem_u32(&v.bar->side[kb & 1]), kb >> 1 & 1, &abort_flag, ctl);
+    const size_t rb = v.first + (size_t)kb * pl.batch;  // the batch's first row
+    const int nrows = v.batch_rows(kb);
+    const float *ls = reinterpret_cast<const float *>(v.mid_at(kb & 1) + v.skew(v.mid, 4, rb));
+    for (int in_batch = 0; in_batch < nrows; in_batch += pl.rows, ++kt) {
+    mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
+    const int n = v.tile_rows(kt);
+    const size_t r0 = rb + in_batch;
+    const T *zs = reinterpret_cast<const T *>(v.tile_at(at) + v.skew(v.Z, v.zrow, r0));
     for (int s0 = 0; s0 < n; s0 += U * t.rows) {
       L x[U];
       float2 z[U][NP];
@@ -666,7 +707,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = s0 + u * t.rows + t.row0;
-        l[u] = r < n ? ls[r] : inf;
+        l[u] = r < n ? ls[in_batch + r] : inf;
         const T *row = zs + r * E;
 #pragma unroll
         for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, l[u] != inf && (p * G + t.lane) * VL < E);
@@ -720,14 +761,18 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
             if ((p * G + t.lane) * VL < E) L::store(p, z[u], l[u] == inf, row, (p * G + t.lane) * VL);
       }
     }
-    if (t.any(*(volatile int *)&abort_flag)) break;  // the stage has been read
-    if (t.thread == 0 && q + (long long)st.stages * hop < ntiles) issue((int)q + st.stages * hop, at);
-    if (++at == st.stages) {
+    gave_up = t.any(*(volatile int *)&abort_flag);  // the tile has been read, and of a batch's last tile the batch
+    if (gave_up) break;
+    if (t.thread == 0 && kt + pl.stages < v.ntiles) v.issue_tile(kt + pl.stages, at);
+    if (++at == pl.stages) {
       at = 0;
       phase ^= 1;
     }
+    }
+    if (gave_up) break;
+    if (t.thread == 0 && kb + 2 < v.nbatches) v.issue_batch(kb + 2, kb & 1);
   }
-  if (q < ntiles && t.thread == 0) drain(full, st, (int)q, hop, ntiles, at, phase);  // a wait ran out
+  if (gave_up && t.thread == 0) v.drain(kb, kt);
 }
 
 // ---------------------------------------------------------------- host ---
@@ -761,50 +806,64 @@ static Spread spread_of(int E, DType dt, bool aligned) {
   return p;
 }
 
-// Tiles and blocks.  mid: bytes of labels (or lse) a row; extra: bytes a block
-// keeps beside its owners' stages.  A block takes its share of an SM's 220 KB
-// of shared memory; an owner's tile is at most a third of its share (three
-// stages), and smaller where the owners of a wave would not all have one, down
-// to a step's rows.
+static int place_of_columns(int E) { return (E * 4 + 15) / 16 * 16; }
+
+// Blocks, and the plan of an owner's rows.  mid: bytes of labels (or lse) a
+// row; extra: bytes a block keeps beside its owners' places.  One wave of
+// blocks (more would leave most of the machine idle in a second one), fewer
+// where an owner would not have a step's rows; a block takes its share of an
+// SM's shared memory, an owner's tiles are as large as leaves three
+// of them.
 struct Grid {
-  Stage st;
+  Plan pl;
   int blocks;  // per problem
   int smem;
 };
 static Grid grid_of(int B, int64_t N, int E, DType dt, int mid, int extra, const Spread &p) {
   Grid g{};
-  const int64_t row = (int64_t)E * dtype_size(dt) + mid + 1, wave = 148 * p.resident / B > 0 ? 148 * p.resident / B : 1;
-  const int64_t room = (220 * 1024 / p.resident - extra - 1024) / p.owners;
-  int64_t R = (room / 3 - 3 * 48) / (row + 3), share = (N + wave * p.owners - 1) / (wave * p.owners);
-  if (share < p.rows) share = p.rows;
-  if (R > share) R = share;
-  R = R < p.rows ? R : R / p.rows * p.rows;
-  if (R > 1024) R = 1024;
-  if (R < 1) R = 1;
   auto place = [](int64_t bytes) { return (int)((bytes + 30 + 15) / 16 * 16); };  // both ends widened
-  g.st.rows = (int)R;
-  g.st.z = place(R * E * dtype_size(dt));
-  g.st.mid = place(R * mid);
-  g.st.small = place(R);
-  const int64_t tiles = (N + R - 1) / R, per_block = (tiles + p.owners - 1) / p.owners;
-  int64_t stages = (room - g.st.stats()) / g.st.bytes();
-  g.st.stages = (int)(stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages);
-  int64_t nb = wave < per_block ? wave : per_block;
+  const int64_t zrow = (int64_t)E * dtype_size(dt);
+  const int64_t wave = 148 * p.resident / B > 0 ? 148 * p.resident / B : 1;
+  const int64_t room = ((225 * 1024 / p.resident - extra - 2048) / p.owners) / 16 * 16;
+  int64_t share = (N + wave * p.owners - 1) / (wave * p.owners);
+  share = (share + p.rows - 1) / p.rows * p.rows;
   // no team adds over 1,024 rows into one fp32 sum
-  const int64_t steps = (N + p.rows * p.owners - 1) / (p.rows * p.owners) * bal_rows(p.VL * p.P);
-  if (nb * 1024 < steps) nb = (steps + 1023) / 1024;
-  g.blocks = (int)(nb < per_block ? nb : per_block);
-  g.smem = p.owners * (g.st.stages * g.st.bytes() + g.st.stats()) + extra;
+  const int64_t most = 1024 * (p.rows / bal_rows(p.VL * p.P));
+  if (share > most) share = most;
+  // a batch of 32 rows (or the step's; fewer where many labels a row would take
+  // over a third of the room) and the largest tile that leaves three of them;
+  // then the batch whole tiles
+  auto side = [&](int64_t batch) { return 2 * (place(batch * mid) + place(batch)) + (batch * 8 + 15) / 16 * 16; };
+  int64_t batch = p.rows > 32 ? p.rows : 32;
+  while (batch > 1 && side(batch) > room / 3) batch /= 2;
+  int64_t rows = ((room - side(batch)) / 3 - 48) / zrow;
+  if (rows > batch) rows = batch;
+  if (rows > share) rows = share;
+  rows = rows < p.rows ? rows : rows / p.rows * p.rows;
+  if (rows < 1) rows = 1;
+  batch = batch / rows * rows;
+  g.pl.share = (int)share;
+  g.pl.rows = (int)rows;
+  g.pl.z = place(rows * zrow);
+  g.pl.batch = (int)batch;
+  g.pl.mid = place(batch * mid);
+  g.pl.small = place(batch);
+  const int64_t stages = (room - side(batch)) / g.pl.z, tiles = (share + rows - 1) / rows;
+  g.pl.stages = (int)(stages < 2 ? 2 : stages > kMaxStages ? kMaxStages : stages);
+  if (g.pl.stages > tiles) g.pl.stages = (int)tiles;
+  g.blocks = (int)((N + share * p.owners - 1) / (share * p.owners));
+  g.smem = p.owners * g.pl.bytes();
+  if (g.smem < extra) g.smem = extra;  // the column sums' turn
+  g.smem += extra;
   return g;
 }
 
 static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 static size_t parts_bytes(int B, int64_t N, int E, DType dt, bool aligned) {
-  // the most labels a row make the smallest tiles and so the most blocks
-  const size_t parts = (size_t)B * grid_of(B, N, E, dt, 4 * kMaxBalanceM, 8 * E, spread_of(E, dt, aligned)).blocks;
+  const size_t parts = (size_t)B * grid_of(B, N, E, dt, 4, place_of_columns(E), spread_of(E, dt, aligned)).blocks;  // for any M
   return 2 * al256(parts * E * 4) + al256(parts * 4);
 }
-// Enough for either alignment of Z and any M.
+// Enough for either alignment of Z.
 size_t balance_workspace_bytes(int B, int64_t N, int E, DType dt) {
   const size_t a = parts_bytes(B, N, E, dt, true), u = parts_bytes(B, N, E, dt, false);
   return a > u ? a : u;
@@ -833,7 +892,7 @@ template <typename T, typename F> static void with_spread(const Spread &p, F f) 
 
 template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void *ws, DevCtl ctl, cudaStream_t s) {
   const Spread p = spread_of(a.E, a.dt, (uintptr_t)a.Z % 16 == 0);
-  const Grid g = grid_of(a.B, a.N, a.E, a.dt, 4 * a.M, 8 * a.E, p);
+  const Grid g = grid_of(a.B, a.N, a.E, a.dt, 4 * a.M, place_of_columns(a.E), p);
   const int nb = g.blocks;
   const size_t parts = (size_t)a.B * nb;
   float *psum = (float *)ws;
@@ -846,7 +905,7 @@ template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void
     e = g.smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem) : cudaSuccess;
     if (e == cudaSuccess)
       e = launch_chained(kernel, dim3(nb, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.ids, a.mask, a.B, a.N, a.E,
-                         a.M, p.logg, g.st, a.lse, psum, csum, tsum, out, ctl);
+                         a.M, p.logg, g.pl, a.lse, psum, csum, tsum, out, ctl);
   });
   count_launches(1);
   if (e != cudaSuccess || nb == 1) return e;
@@ -883,7 +942,7 @@ template <typename T> static cudaError_t balance_grad_from(const BalanceGradArgs
     e = g.smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem) : cudaSuccess;
     if (e == cudaSuccess)
       e = launch_chained(kernel, dim3(g.blocks, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.counts, a.tokens,
-                         a.lse, a.gloss, a.B, a.N, a.E, a.M, a.coef, p.logg, g.st, (T *)a.dZ, ctl);
+                         a.lse, a.gloss, a.B, a.N, a.E, a.M, a.coef, p.logg, g.pl, (T *)a.dZ, ctl);
   });
   return e;
 }
