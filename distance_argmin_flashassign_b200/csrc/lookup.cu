@@ -247,8 +247,11 @@ cudaError_t launch_lookup(const LookupArgs &a, int *status, cudaStream_t s) {
 // 148 SMs hold 113,664 lanes of the row-sum kernel (3 blocks of 256).
 static int grad_rows_R(long long rows, int row_bytes) {
   const long long pieces = rows * ((row_bytes + 15) / 16);
-  long long R = (pieces + 113663) / 113664;
-  R = (R + 7) / 8 * 8;
+#ifndef GF
+#define GF 1
+#endif
+  long long R = (pieces + 113664 * GF - 1) / (113664 * GF);
+  R = (R + 31) / 32 * 32;
   return (int)(R < 32 ? 32 : R > 512 ? 512 : R);
 }
 
@@ -289,24 +292,36 @@ __device__ __forceinline__ void put_grad(void *dT, int dt, size_t at, float *v, 
 // columns.  A segment (run of one label) inside the chunk goes straight to
 // dT; the pieces of segments that cross the chunk's ends go to the chunk's
 // two partial rows (0: the piece that starts the chunk, 1: the one that ends
-// it).  `none` is the key of the points left out.
-constexpr int kGradRows = 8;  // rows in flight per worker
+// it).  `none` is the key of the points left out.  As in the lookup, the lanes
+// hold W positions' keys and rows, the next W are on their way, and the rows
+// of a step are loaded before those of the step before are added.
+#ifndef GU
+#define GU 4
+#define GB 3
+#endif
+constexpr int kGradRows = GU;  // rows of a step
 template <typename T, int VB, int W>
-__global__ void __launch_bounds__(256, 3) grad_sum_kernel(const T *__restrict__ dY, int D,
+__global__ void __launch_bounds__(256, GB) grad_sum_kernel(const T *__restrict__ dY, int D,
                                                           const int32_t *__restrict__ skeys,
                                                           const int32_t *__restrict__ perm, int rows, int none, int R,
                                                           float scale, void *__restrict__ dT, int dt_t, int add,
                                                           float *__restrict__ parts) {
   constexpr int EPL = VB / (int)sizeof(T), U = kGradRows;
+  using V = typename Raw<VB>::type;
   const int lw = threadIdx.x % W;
   const int col = (blockIdx.y * W + lw) * EPL;
   const bool mine = col < D;
+  const T *Yc = dY + col;
   const long long wq = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
   wait_prior_grid();
   const long long p0l = wq * R;
   const int p0 = p0l < rows ? (int)p0l : rows;
   const int p1 = rows - p0 < R ? rows : p0 + R;
   const bool live = p0 < p1;
+  auto key_at = [&](long long pos) { return pos < p1 ? skeys[pos] : none; };
+  auto row_at = [&](long long pos) { return pos < p1 ? perm[pos] : 0; };
+  int kn = key_at((long long)p0 + lw), rn = row_at((long long)p0 + lw);
+  int kx = key_at((long long)p0 + W + lw), rx = row_at((long long)p0 + W + lw);
   int cur = live ? skeys[p0] : none, s = p0;
   const bool split_start = live && p0 > 0 && skeys[p0 - 1] == cur;
   const bool split_end = live && p1 < rows && skeys[p1] == skeys[p1 - 1];
@@ -320,78 +335,149 @@ __global__ void __launch_bounds__(256, 3) grad_sum_kernel(const T *__restrict__ 
     else
       put_grad<EPL>(dT, dt_t, (size_t)k * D + col, a, scale, add);
   };
-  const int nb = (R + U - 1) / U;  // the same for every worker: shuffles stay converged
-  for (int bt = 0; bt < nb; ++bt) {
-    const int b0 = p0 + bt * U;
-    const bool in = lw < U && b0 + lw < p1;
-    const int mk = in ? skeys[b0 + lw] : none, mr = in ? perm[b0 + lw] : 0;
-    typename Raw<VB>::type v[U];
-    int ku[U];
+  struct Step {
+    V v[U];
+    int k[U];
+  } x, y;
+  auto load = [&](Step &n, int j) {  // step j of the W positions at hand
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = __shfl_sync(0xffffffffu, mr, u, W);
-      ku[u] = __shfl_sync(0xffffffffu, mk, u, W);
-      if (ku[u] != none && mine) v[u] = ld_raw<VB>(dY + (size_t)row * D + col);
+      const int row = __shfl_sync(0xffffffffu, rn, j * U + u, W);
+      n.k[u] = __shfl_sync(0xffffffffu, kn, j * U + u, W);
+      if (n.k[u] != none && mine) n.v[u] = ld_raw<VB>(Yc + (size_t)(unsigned)row * (unsigned)D);
+    }
+  };
+  int j = 0, base = p0;  // the next step's place among the W positions; the step to add
+  auto turn = [&](Step &c, Step &n) {
+    if (++j == W / U) {
+      j = 0;
+      kn = kx;
+      rn = rx;
+      load(n, 0);
+      kx = key_at((long long)base + U + W + lw);
+      rx = row_at((long long)base + U + W + lw);
+    } else {
+      load(n, j);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (b0 + u >= p1) break;
-      if (ku[u] != cur) {
-        flush(cur, s, b0 + u);
-        cur = ku[u];
-        s = b0 + u;
+      if (base + u < p1) {
+        if (c.k[u] != cur) {
+          flush(cur, s, base + u);
+          cur = c.k[u];
+          s = base + u;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) a[i] = 0.f;
-      }
-      if (cur != none && mine) {
-        float f[EPL];
-        unpack_raw<T, VB>(v[u], f);
+          for (int i = 0; i < EPL; ++i) a[i] = 0.f;
+        }
+        if (cur != none && mine) {
+          float f[EPL];
+          unpack_raw<T, VB>(c.v[u], f);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) a[i] += f[i];
+          for (int i = 0; i < EPL; ++i) a[i] += f[i];
+        }
       }
     }
+    base += U;
+  };
+  load(x, 0);
+  for (int i = 0; i < R; i += 2 * U) {  // the same for every worker: shuffles stay converged
+    turn(x, y);
+    turn(y, x);
   }
   if (live) flush(cur, s, p1);
 }
 
-// One block per chunk and 128 columns: if a segment starts in this chunk and
-// runs past its end, its partial rows are added -- warp w takes pieces w,
-// w + 8, ..., then the eight sums in warp order -- and written.
-__global__ void __launch_bounds__(256) grad_join_kernel(const int32_t *__restrict__ skeys, int rows, int none, int R,
-                                                        int D, const float *__restrict__ parts, float scale,
-                                                        void *__restrict__ dT, int dt_t, int add) {
-  __shared__ float red[8][128];
-  wait_prior_grid();
-  const int q = blockIdx.x, p0 = q * R;
-  if (rows - p0 <= R) return;  // the last chunk: nothing runs past it
-  const int p1 = p0 + R, k = skeys[p1 - 1];
-  if (k == none || skeys[p1] != k) return;
-  if (p0 > 0 && skeys[p0 - 1] == k) return;  // started in an earlier chunk
-  const int first = skeys[p0] == k ? 0 : 1;
-  const int nchunks = (rows + R - 1) / R;
-  // pieces: this chunk's and those of the following chunks that start with k
-  // (a label's positions are consecutive, so these chunks are too)
-  int np = 1;
-  for (int more = 256; more == 256; np += more) {
-    const int i = q + np + (int)threadIdx.x;
-    more = __syncthreads_count(i < nchunks && skeys[i < nchunks ? i * R : 0] == k);
-  }
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c0 = blockIdx.y * 128;
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = w; i < np; i += 8) {
-    const float *row = parts + ((size_t)(q + i) * 2 + (i == 0 ? first : 0)) * D + c0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (c0 + lane + 32 * j < D) t[j] += row[lane + 32 * j];
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) red[w][lane + 32 * j] = t[j];
+// A segment that starts in chunk q and runs past its end is joined from its
+// partial rows here, by the warp that looks at chunk q; where it has more than
+// kHotPieces of them, by the block's 32 warps afterwards (warp w adds pieces
+// w, w + 32, ..., then the 32 sums are added in warp order).  blockIdx.y:
+// slice of kJoinCols columns.
+constexpr int kHotPieces = 16, kJoinCols = 512;
+__global__ void __launch_bounds__(1024) grad_join_kernel(const int32_t *__restrict__ skeys, int rows, int none, int R,
+                                                         int D, const float *__restrict__ parts, float scale,
+                                                         void *__restrict__ dT, int dt_t, int add) {
+  __shared__ float red[32][129];
+  __shared__ int hot_q[32], hot_np[32], nhot;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int nchunks = (rows + R - 1) / R, q = blockIdx.x * 32 + w;
+  const int c0 = blockIdx.y * kJoinCols, c1 = min(D, c0 + kJoinCols);
+  if (threadIdx.x == 0) nhot = 0;
   __syncthreads();
-  const int c = threadIdx.x;
-  if (c < 128 && c0 + c < D) {
-    float sum[1] = {0.f};
-    for (int ww = 0; ww < 8; ++ww) sum[0] += red[ww][c];
-    put_grad<1>(dT, dt_t, (size_t)k * D + c0 + c, sum, scale, add);
+  wait_prior_grid();
+  // pieces of the segment that ends chunk q: this chunk's and those of the
+  // following chunks that start with its label (a label's positions are
+  // consecutive, so these chunks are too); 1 where it does not start here or
+  // does not run past the end
+  int np = 1, k = none;
+  if (q < nchunks - 1) {
+    const int p0 = q * R, p1 = p0 + R;
+    k = skeys[p1 - 1];
+    const int after = skeys[p1], before = p0 > 0 ? skeys[p0 - 1] : -1;
+    if (k != none && after == k && before != k) {
+      // the last such chunk, by 32-fold search: chunk lo starts with k, chunk hi does not
+      int lo = q + 1, hi = nchunks;
+      while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = lo + step * (lane + 1);
+        const unsigned in = __ballot_sync(0xffffffffu, i < hi && skeys[i < hi ? i * R : 0] == k);
+        const int n = __popc(in);
+        hi = min(hi, lo + step * (n + 1));
+        lo += step * n;
+      }
+      np = lo - q + 1;
+    }
+  }
+  auto piece = [&](int q, int first, int i) { return parts + ((size_t)(q + i) * 2 + (i == 0 ? first : 0)) * D; };
+  // adds pieces from, from + by, ... of columns c + lane + 32 j, four pieces loaded at a time
+  auto add_pieces = [&](float *t, int q, int first, int from, int by, int np, int c) {
+    for (int i0 = from; i0 < np; i0 += 4 * by) {
+      float v[4][4];
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        const int i = i0 + ii * by;
+        const float *row = piece(q, first, i < np ? i : 0) + c + lane;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) v[ii][jj] = i < np && c + lane + 32 * jj < c1 ? row[32 * jj] : 0.f;
+      }
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii)
+        if (i0 + ii * by < np) {
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) t[jj] += v[ii][jj];
+        }
+    }
+  };
+  if (np > kHotPieces) {
+    if (lane == 0) {
+      const int i = atomicAdd(&nhot, 1);  // any order: each is summed by itself
+      hot_q[i] = q;
+      hot_np[i] = np;
+    }
+  } else if (np > 1) {
+    const int first = skeys[q * R] == k ? 0 : 1;
+    for (int c = c0; c < c1; c += 128) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      add_pieces(t, q, first, 0, 1, np, c);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj)
+        if (c + lane + 32 * jj < c1) put_grad<1>(dT, dt_t, (size_t)k * D + c + lane + 32 * jj, t + jj, scale, add);
+    }
+  }
+  __syncthreads();
+  for (int h = 0; h < nhot; ++h) {
+    const int hq = hot_q[h], hk = skeys[hq * R + R - 1], first = skeys[hq * R] == hk ? 0 : 1;
+    for (int c = c0; c < c1; c += 128) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      add_pieces(t, hq, first, w, 32, hot_np[h], c);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) red[w][lane + 32 * jj] = t[jj];
+      __syncthreads();
+      if (threadIdx.x < 128 && c + threadIdx.x < c1) {
+        float sum[1] = {0.f};
+        for (int ww = 0; ww < 32; ++ww) sum[0] += red[ww][threadIdx.x];
+        put_grad<1>(dT, dt_t, (size_t)hk * D + c + threadIdx.x, sum, scale, add);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -448,7 +534,8 @@ cudaError_t launch_lookup_grad(const LookupGradArgs &a, void *ws, int *status, c
   if (a.dt == kF32) launch_grad_from<float>(a, o, n, none, R, parts, s);
   else if (a.dt == kF16) launch_grad_from<__half>(a, o, n, none, R, parts, s);
   else launch_grad_from<__nv_bfloat16>(a, o, n, none, R, parts, s);
-  launch_chained(grad_join_kernel, dim3((n + R - 1) / R, (a.D + 127) / 128), dim3(256), 0, s, o.skeys, n, none, R, a.D,
+  const int nchunks = (n + R - 1) / R;
+  launch_chained(grad_join_kernel, dim3((nchunks + 31) / 32, (a.D + kJoinCols - 1) / kJoinCols), dim3(1024), 0, s, o.skeys, n, none, R, a.D,
                  parts, a.scale, a.dT, (int)a.dt_t, a.accumulate);
   count_launches(2);
   return cudaGetLastError();
