@@ -255,6 +255,12 @@ static int grad_rows_R(long long rows, int row_bytes) {
   return (int)(R < 32 ? 32 : R > 512 ? 512 : R);
 }
 
+__device__ __forceinline__ void add2(float *a, const float *b) {  // two fp32 additions an instruction
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a[0]), "+f"(a[1])
+      : "f"(b[0]), "f"(b[1]));
+}
 // Writes scale v (+ the row's own values) at columns [col, col + n) of row k.
 template <int n>
 __device__ __forceinline__ void put_grad(void *dT, int dt, size_t at, float *v, float scale, bool add) {
@@ -320,8 +326,10 @@ __global__ void __launch_bounds__(256, GB) grad_sum_kernel(const T *__restrict__
   const bool live = p0 < p1;
   auto key_at = [&](long long pos) { return pos < p1 ? skeys[pos] : none; };
   auto row_at = [&](long long pos) { return pos < p1 ? perm[pos] : 0; };
+  // the W positions at hand and the next W: key, and row (-1: left out)
   int kn = key_at((long long)p0 + lw), rn = row_at((long long)p0 + lw);
   int kx = key_at((long long)p0 + W + lw), rx = row_at((long long)p0 + W + lw);
+  if (kn == none) rn = -1;
   int cur = live ? skeys[p0] : none, s = p0;
   const bool split_start = live && p0 > 0 && skeys[p0 - 1] == cur;
   const bool split_end = live && p1 < rows && skeys[p1] == skeys[p1 - 1];
@@ -335,45 +343,61 @@ __global__ void __launch_bounds__(256, GB) grad_sum_kernel(const T *__restrict__
     else
       put_grad<EPL>(dT, dt_t, (size_t)k * D + col, a, scale, add);
   };
+  auto add_row = [&](const V &v) {
+    float f[EPL];
+    unpack_raw<T, VB>(v, f);
+    if constexpr (EPL == 1) {
+      a[0] += f[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 2) add2(a + i, f + i);
+    }
+  };
   struct Step {
     V v[U];
-    int k[U];
+    int keys, first, last;  // the W positions' keys it is among; its first and last position's
   } x, y;
   auto load = [&](Step &n, int j) {  // step j of the W positions at hand
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int row = __shfl_sync(0xffffffffu, rn, j * U + u, W);
-      n.k[u] = __shfl_sync(0xffffffffu, kn, j * U + u, W);
-      if (n.k[u] != none && mine) n.v[u] = ld_raw<VB>(Yc + (size_t)(unsigned)row * (unsigned)D);
+      if (row >= 0 && mine) n.v[u] = ld_raw<VB>(Yc + (size_t)(unsigned)row * (unsigned)D);
     }
+    n.keys = kn;
+    n.first = __shfl_sync(0xffffffffu, kn, j * U, W);
+    n.last = __shfl_sync(0xffffffffu, kn, j * U + U - 1, W);
   };
-  int j = 0, base = p0;  // the next step's place among the W positions; the step to add
+  int j = 0, base = p0;  // the step to add: its place among its W positions, its first position
   auto turn = [&](Step &c, Step &n) {
+    const int jc = j;
     if (++j == W / U) {
       j = 0;
       kn = kx;
-      rn = rx;
+      rn = kx == none ? -1 : rx;
       load(n, 0);
       kx = key_at((long long)base + U + W + lw);
       rx = row_at((long long)base + U + W + lw);
     } else {
       load(n, j);
     }
+    // a label's positions are consecutive: equal ends, one label in between
+    if (__all_sync(0xffffffffu, c.first == cur && c.last == cur && cur != none)) {
+      if (mine)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (base + u < p1) {
-        if (c.k[u] != cur) {
-          flush(cur, s, base + u);
-          cur = c.k[u];
-          s = base + u;
+        for (int u = 0; u < U; ++u) add_row(c.v[u]);
+    } else {
 #pragma unroll
-          for (int i = 0; i < EPL; ++i) a[i] = 0.f;
-        }
-        if (cur != none && mine) {
-          float f[EPL];
-          unpack_raw<T, VB>(c.v[u], f);
+      for (int u = 0; u < U; ++u) {
+        const int k = __shfl_sync(0xffffffffu, c.keys, jc * U + u, W);
+        if (base + u < p1) {
+          if (k != cur) {
+            flush(cur, s, base + u);
+            cur = k;
+            s = base + u;
 #pragma unroll
-          for (int i = 0; i < EPL; ++i) a[i] += f[i];
+            for (int i = 0; i < EPL; ++i) a[i] = 0.f;
+          }
+          if (cur != none && mine) add_row(c.v[u]);
         }
       }
     }
