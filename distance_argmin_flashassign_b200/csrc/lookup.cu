@@ -247,11 +247,8 @@ cudaError_t launch_lookup(const LookupArgs &a, int *status, cudaStream_t s) {
 // 148 SMs hold 113,664 lanes of the row-sum kernel (3 blocks of 256).
 static int grad_rows_R(long long rows, int row_bytes) {
   const long long pieces = rows * ((row_bytes + 15) / 16);
-#ifndef GF
-#define GF 1
-#endif
-  long long R = (pieces + 113664 * GF - 1) / (113664 * GF);
-  R = (R + 31) / 32 * 32;
+  long long R = (pieces + 113663) / 113664;
+  R = (R + 7) / 8 * 8;
   return (int)(R < 32 ? 32 : R > 512 ? 512 : R);
 }
 
@@ -301,13 +298,9 @@ __device__ __forceinline__ void put_grad(void *dT, int dt, size_t at, float *v, 
 // it).  `none` is the key of the points left out.  As in the lookup, the lanes
 // hold W positions' keys and rows, the next W are on their way, and the rows
 // of a step are loaded before those of the step before are added.
-#ifndef GU
-#define GU 4
-#define GB 3
-#endif
-constexpr int kGradRows = GU;  // rows of a step
+constexpr int kGradRows = 4;  // rows of a step
 template <typename T, int VB, int W>
-__global__ void __launch_bounds__(256, GB) grad_sum_kernel(const T *__restrict__ dY, int D,
+__global__ void __launch_bounds__(256, 3) grad_sum_kernel(const T *__restrict__ dY, int D,
                                                           const int32_t *__restrict__ skeys,
                                                           const int32_t *__restrict__ perm, int rows, int none, int R,
                                                           float scale, void *__restrict__ dT, int dt_t, int add,
