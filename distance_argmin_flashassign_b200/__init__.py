@@ -19,7 +19,6 @@ A 3-D ``X`` (B x N x D) selects the batched entry points.  Failures raise
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -131,7 +130,7 @@ def _dtype(X: torch.Tensor) -> int:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape, device) -> None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
@@ -350,34 +349,36 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _book_stream(device, stream):
-    """(the raw stream of a call on ``device``, the context for its allocations and launches)"""
+def _elsewhere(device, stream):
+    """None if ``device`` is the current one and no stream is given; else the
+    context in which that is so (the calls then start over inside it)."""
     if device.type != "cuda":
         raise ValueError(f"expected CUDA tensors, got {device}")
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
-        if device.index == torch.cuda.current_device():
-            return raw, contextlib.nullcontext()
-        return raw, torch.cuda.device(device)
+        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
         raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
-def _book_workspace(workspace, size, device):
-    """The workspace argument of a call that needs ``size`` bytes: the caller's
-    tensor, none (the library's scratch), or under stream capture, where the
-    library has none to give, one of the graph's own pool."""
-    if workspace is not None:
-        if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
-            raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
-        return workspace, workspace.numel()
-    if torch.cuda.is_current_stream_capturing():
-        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device=device)
-        return workspace, workspace.numel()
-    return None, 0
+# the current stream of a device as a plain number; the second form makes a Stream object (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _book_workspace(workspace, size, like):
+    """(address, bytes) of the workspace of a call that needs ``size()`` bytes:
+    the caller's tensor, none (the library's scratch), or under stream
+    capture, where the library has none to give, one of the graph's own pool."""
+    if workspace is None:
+        if not torch.cuda.is_current_stream_capturing():
+            return None, 0
+        workspace = like.new_empty(max(size(), 1), dtype=torch.uint8)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != like.device:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {like.device}")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def fk_lookup(T, ids, scale=1.0, Y=None, dtype=None, stream=None):
@@ -387,15 +388,19 @@ def fk_lookup(T, ids, scale=1.0, Y=None, dtype=None, stream=None):
     B, K, D, bat = _dims(T)
     N = ids.shape[-1] if ids.dim() else 0
     lead = (B, N) if bat else (N,)
-    dt = _dtype(T)
-    _need(T, "T", T.dtype, T.shape, T.device)
-    _need(ids, "ids", torch.int32, lead, T.device)
-    raw, ctx = _book_stream(T.device, stream)
-    with ctx:
-        if Y is None:
-            Y = torch.empty(lead + (D,), dtype=dtype or T.dtype, device=T.device)
-        _need(Y, "Y", dtype or Y.dtype, lead + (D,), T.device)
-        _check(lib.fk_lookup(T.data_ptr(), B, K, D, dt, ids.data_ptr(), N, scale, Y.data_ptr(), _dtype(Y), raw))
+    dt, dev = _dtype(T), T.device
+    _need(T, "T", T.dtype, T.shape, dev)
+    _need(ids, "ids", torch.int32, lead, dev)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return fk_lookup(T, ids, scale, Y, dtype)
+    if Y is None:
+        Y = T.new_empty(lead + (D,), dtype=dtype)
+    else:
+        _need(Y, "Y", dtype or Y.dtype, lead + (D,), dev)
+    _check(lib.fk_lookup(T.data_ptr(), B, K, D, dt, ids.data_ptr(), N, scale, Y.data_ptr(), _dtype(Y),
+                         _raw_stream(dev.index)))
     return Y
 
 
@@ -406,19 +411,22 @@ def fk_lookup_grad(dY, ids, K, scale=1.0, dT=None, dtype=None, accumulate=False,
     dY N x D with ids N, or B x N x D with ids B x N."""
     B, N, D, bat = _dims(dY)
     shape = (B, K, D) if bat else (K, D)
-    dt = _dtype(dY)
-    _need(dY, "dY", dY.dtype, dY.shape, dY.device)
-    _need(ids, "ids", torch.int32, ((B, N) if bat else (N,)), dY.device)
+    dt, dev = _dtype(dY), dY.device
+    _need(dY, "dY", dY.dtype, dY.shape, dev)
+    _need(ids, "ids", torch.int32, (B, N) if bat else (N,), dev)
     if accumulate and dT is None:
         raise ValueError("accumulate needs dT")
-    raw, ctx = _book_stream(dY.device, stream)
-    with ctx:
-        if dT is None:
-            dT = torch.empty(shape, dtype=dtype or torch.float32, device=dY.device)
-        _need(dT, "dT", dtype or dT.dtype, shape, dY.device)
-        ws, nws = _book_workspace(workspace, lambda: lib.fk_lookup_grad_workspace(B, N, D, dt, K), dY.device)
-        _check(lib.fk_lookup_grad(dY.data_ptr(), B, N, D, dt, ids.data_ptr(), K, scale, dT.data_ptr(), _dtype(dT),
-                                  int(bool(accumulate)), _addr(ws), nws, raw))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return fk_lookup_grad(dY, ids, K, scale, dT, dtype, accumulate, workspace)
+    if dT is None:
+        dT = dY.new_empty(shape, dtype=dtype or torch.float32)
+    else:
+        _need(dT, "dT", dtype or dT.dtype, shape, dev)
+    ws, nws = _book_workspace(workspace, lambda: lib.fk_lookup_grad_workspace(B, N, D, dt, K), dY)
+    _check(lib.fk_lookup_grad(dY.data_ptr(), B, N, D, dt, ids.data_ptr(), K, scale, dT.data_ptr(), _dtype(dT),
+                              1 if accumulate else 0, ws, nws, _raw_stream(dev.index)))
     return dT
 
 
@@ -431,29 +439,31 @@ def fk_balance(Z, ids, mask=None, coef=1.0, loss=None, counts=None, tokens=None,
     capacity limit need."""
     B, N, E, bat = _dims(Z)
     lead, top = ((B, N), (B,)) if bat else ((N,), ())
-    dev = Z.device
-    dt = _dtype(Z)
+    dt, dev = _dtype(Z), Z.device
     M = 1 if ids.dim() == len(lead) else ids.shape[-1]
     _need(Z, "Z", Z.dtype, Z.shape, dev)
     _need(ids, "ids", torch.int32, lead if ids.dim() == len(lead) else lead + (M,), dev)
     if mask is not None:
         _need(mask, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool, lead, dev)
-    raw, ctx = _book_stream(dev, stream)
-    with ctx:
-        def out(t, name, dtype, shape):
-            if t is None:
-                return torch.empty(shape, dtype=dtype, device=dev)
-            _need(t, name, dtype, shape, dev)
-            return t
-        loss = out(loss, "loss", torch.float32, top)
-        counts = out(counts, "counts", torch.int32, top + (E,))
-        tokens = out(tokens, "tokens", torch.int32, top)
-        meanp = out(meanp, "meanp", torch.float32, top + (E,))
-        lse = out(lse, "lse", torch.float32, lead)
-        ws, nws = _book_workspace(workspace, lambda: lib.fk_balance_workspace(B, N, E, dt), dev)
-        _check(lib.fk_balance(Z.data_ptr(), B, N, E, dt, ids.data_ptr(), M, _addr(mask), coef, loss.data_ptr(),
-                              counts.data_ptr(), tokens.data_ptr(), meanp.data_ptr(), lse.data_ptr(), _addr(ws), nws,
-                              raw))
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return fk_balance(Z, ids, mask, coef, loss, counts, tokens, meanp, lse, workspace)
+
+    def out(t, name, dtype, shape):
+        if t is None:
+            return Z.new_empty(shape, dtype=dtype)
+        _need(t, name, dtype, shape, dev)
+        return t
+    loss = out(loss, "loss", torch.float32, top)
+    counts = out(counts, "counts", torch.int32, top + (E,))
+    tokens = out(tokens, "tokens", torch.int32, top)
+    meanp = out(meanp, "meanp", torch.float32, top + (E,))
+    lse = out(lse, "lse", torch.float32, lead)
+    ws, nws = _book_workspace(workspace, lambda: lib.fk_balance_workspace(B, N, E, dt), Z)
+    _check(lib.fk_balance(Z.data_ptr(), B, N, E, dt, ids.data_ptr(), M, _addr(mask), coef, loss.data_ptr(),
+                          counts.data_ptr(), tokens.data_ptr(), meanp.data_ptr(), lse.data_ptr(), ws, nws,
+                          _raw_stream(dev.index)))
     return loss, counts, tokens, meanp, lse
 
 
@@ -463,20 +473,23 @@ def fk_balance_grad(Z, counts, tokens, lse, M, coef=1.0, gloss=None, dZ=None, st
     loss) is the loss's own gradient, 1 by default.  ``dZ`` may be Z."""
     B, N, E, bat = _dims(Z)
     lead, top = ((B, N), (B,)) if bat else ((N,), ())
-    dev = Z.device
+    dt, dev = _dtype(Z), Z.device
     _need(Z, "Z", Z.dtype, Z.shape, dev)
     _need(counts, "counts", torch.int32, top + (E,), dev)
     _need(tokens, "tokens", torch.int32, top, dev)
     _need(lse, "lse", torch.float32, lead, dev)
     if gloss is not None:
         _need(gloss, "gloss", torch.float32, top, dev)
-    raw, ctx = _book_stream(dev, stream)
-    with ctx:
-        if dZ is None:
-            dZ = torch.empty_like(Z)
+    away = _elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return fk_balance_grad(Z, counts, tokens, lse, M, coef, gloss, dZ)
+    if dZ is None:
+        dZ = torch.empty_like(Z)
+    else:
         _need(dZ, "dZ", Z.dtype, Z.shape, dev)
-        _check(lib.fk_balance_grad(Z.data_ptr(), B, N, E, _dtype(Z), counts.data_ptr(), tokens.data_ptr(),
-                                   lse.data_ptr(), M, coef, _addr(gloss), dZ.data_ptr(), raw))
+    _check(lib.fk_balance_grad(Z.data_ptr(), B, N, E, dt, counts.data_ptr(), tokens.data_ptr(), lse.data_ptr(), M, coef,
+                               _addr(gloss), dZ.data_ptr(), _raw_stream(dev.index)))
     return dZ
 
 

@@ -13,6 +13,7 @@
 // leave their sums in partial rows that a second kernel adds in block order.
 // Counts are integers, so the shared-memory atomics that make them do not
 // change the result.
+#include <atomic>
 #include <type_traits>
 
 #include "chain.cuh"
@@ -160,6 +161,7 @@ template <typename T, int VL, int P> struct Lane {
   }
 };
 
+constexpr int kMaxSmem = 220 * 1024;  // of a block of these kernels, beside some 1 KB of static shared memory
 constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
 constexpr int kBalLane = 32, kBalSome = 16;  // columns a lane holds at most, and where a warp has lanes to spare
 // Lanes of a team, as a power of two, where the kernel is compiled for them:
@@ -869,6 +871,19 @@ size_t balance_workspace_bytes(int B, int64_t N, int E, DType dt) {
   return a > u ? a : u;
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory; `allowed` remembers per
+// device what it may have already.
+template <typename K> static cudaError_t allow_smem(K kernel, int bytes, std::atomic<int> *allowed) {
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && allowed[dev].load() >= bytes)) return e;
+  // the most that any call may ask for, so that calls from two threads do not undo one another
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess && dev < 64) allowed[dev].store(kMaxSmem);
+  return e;
+}
+
 // Calls f with the spread's template arguments: every spread that spread_of
 // makes is listed.
 template <typename T, typename F> static void with_spread(const Spread &p, F f) {
@@ -902,7 +917,8 @@ template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void
   cudaError_t e = cudaErrorNotSupported;
   with_spread<T>(p, [&](auto vl, auto np, auto lg) {
     const auto kernel = balance_rows_kernel<T, decltype(vl)::value, decltype(np)::value, decltype(lg)::value>;
-    e = g.smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem) : cudaSuccess;
+    static std::atomic<int> allowed[64];
+    e = allow_smem(kernel, g.smem, allowed);
     if (e == cudaSuccess)
       e = launch_chained(kernel, dim3(nb, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.ids, a.mask, a.B, a.N, a.E,
                          a.M, p.logg, g.pl, a.lse, psum, csum, tsum, out, ctl);
@@ -939,7 +955,8 @@ template <typename T> static cudaError_t balance_grad_from(const BalanceGradArgs
   cudaError_t e = cudaErrorNotSupported;
   with_spread<T>(p, [&](auto vl, auto np, auto lg) {
     const auto kernel = balance_grad_kernel<T, decltype(vl)::value, decltype(np)::value, decltype(lg)::value>;
-    e = g.smem > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem) : cudaSuccess;
+    static std::atomic<int> allowed[64];
+    e = allow_smem(kernel, g.smem, allowed);
     if (e == cudaSuccess)
       e = launch_chained(kernel, dim3(g.blocks, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.counts, a.tokens,
                          a.lse, a.gloss, a.B, a.N, a.E, a.M, a.coef, p.logg, g.pl, (T *)a.dZ, ctl);
