@@ -13,6 +13,10 @@ namespace fk {
 // writes are visible.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next grid of the chain start once every block of this one has come
+// here or ended; without it that is when every block has ended.
+__device__ __forceinline__ void let_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 template <typename... KArgs, typename... Args>
 static cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                   Args... args) {

@@ -119,17 +119,20 @@ cudaError_t launch_assign_tc(DType dt, const void *X, const void *C, const float
 
 // ---- label_sort.cu: stable sort of points by label -------------------------
 // The B*N points in label order: skeys[j] = b*K + label of the j-th, perm[j]
-// its row b*N + i; points of one label in ascending row order.  drop: labels
-// outside [0, K) are left out -- they get the key B*K and lie behind the rest
-// (behind their problem's rest when B > 1) -- and -1 is not an error; without
-// drop they count as 0.
+// its row b*N + i; points of one label in ascending row order.  Labels outside
+// [0, K) count as 0 and are recorded in `status`.
 struct LabelSort {
   const int32_t *skeys, *perm;
 };
 size_t label_sort_bytes(int64_t Ntot, int64_t Ktot, int B, bool drop);
-// ws of label_sort_bytes(B * N, B * K, B, drop), where the result lies; B * N > 0.
-cudaError_t launch_label_sort(const int32_t *labels, int B, int N, int K, bool drop, void *ws, int *status,
-                              cudaStream_t s, LabelSort *out);
+// ws of label_sort_bytes(B * N, B * K, B, false), where the result lies; B * N > 0.
+cudaError_t launch_label_sort(const int32_t *labels, int B, int N, int K, void *ws, int *status, cudaStream_t s,
+                              LabelSort *out);
+// The same with labels outside [0, K) left out: they get the key B*K and lie
+// behind the rest (behind their problem's rest when B > 1); -1 is not an
+// error.  Zero-fills fill_bytes bytes at `fill` on the way.
+cudaError_t launch_label_sort_drop(const int32_t *labels, int B, int N, int K, void *ws, int *status, cudaStream_t s,
+                                   LabelSort *out, void *fill, size_t fill_bytes);
 
 // ---- lookup.cu: codebook rows by label, and the codebook's gradient --------
 constexpr int kMaxLookupD = 16384;  // largest D of these calls

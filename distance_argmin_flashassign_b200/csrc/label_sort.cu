@@ -345,8 +345,248 @@ __global__ void __launch_bounds__(kSortThreads) radix_scatter_kernel(
 }
 
 
-// ---------------------------------------------------------------- host ---
 static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
+
+// ------------------------------------------------- one launch, few points --
+// Up to kFewPoints points are sorted by one cluster of CTAs in one launch (a
+// whole gradient of 32,768 x 64 bf16 in a replayed graph: 33 us with 60,000
+// labels, 39 us with the kernels above; with 65,536 points, eight CTAs are too
+// few: 44 us and 39 us): the
+// three kernels of a pass become two cluster barriers, the tiles' digit counts
+// are read from the CTAs' shared memory, and the points change CTAs by stores
+// to shared memory.  Digits of at most 9 bits: two passes up to 2^18 keys,
+// three up to 2^22.  Meanwhile an array is zero-filled (the gradient's, whose
+// rows without a point nobody else writes): a little by the grid's other
+// clusters, more by a kernel of its own that runs beside the sort.
+constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewCtas = 8, kFewItems = 8;
+constexpr int kFewPoints = kFewThreads * kFewItems * kFewCtas;  // 32,768
+constexpr size_t kFewFill = size_t(32) << 20;
+constexpr int kFewBits = 9, kFewBins = 1 << kFewBits;
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster2(uint32_t addr, int a, int b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// Zeroes [p, p + n), p aligned to its 2- or 4-byte elements; block `at` of `of`.
+__device__ __forceinline__ void zero_fill(char *p, size_t n, int at, int of) {
+  const size_t head = n < ((16 - (uintptr_t)p % 16) % 16) ? n : (16 - (uintptr_t)p % 16) % 16;
+  const size_t body = (n - head) / 16, tail = n - head - body * 16;
+  if (at == 0) {
+    unsigned short *h = (unsigned short *)p, *t = (unsigned short *)(p + head + body * 16);
+    if (threadIdx.x < head / 2) h[threadIdx.x] = 0;
+    if (threadIdx.x < tail / 2) t[threadIdx.x] = 0;
+  }
+  uint4 *q = (uint4 *)(p + head);
+#pragma unroll 4
+  for (size_t i = (size_t)at * blockDim.x + threadIdx.x; i < body; i += (size_t)of * blockDim.x)
+    q[i] = make_uint4(0, 0, 0, 0);
+}
+
+static int few_smem_bytes(int bins, int items) {
+  return (2 * bins + kFewWarps + kFewWarps * bins + kFewWarps * (bins + 1) + 2 * kFewThreads * items) * 4;
+}
+
+// ITEMS points a thread; CTA c of the first cluster holds positions
+// [c, c + 1) * kFewThreads * ITEMS.
+template <int ITEMS>
+__global__ void __launch_bounds__(kFewThreads) sort_few_kernel(const int32_t *__restrict__ labels, int rows, int N,
+                                                               int K, int B, int npass, int bits, int bins,
+                                                               int32_t *__restrict__ skeys,
+                                                               int32_t *__restrict__ perm, char *fill, size_t fill_bytes,
+                                                               int ncta, int *status) {
+  constexpr int TILE = kFewThreads * ITEMS;
+  extern __shared__ int sh[];
+  wait_prior_grid();
+  let_next_grid();  // fill_kernel, where there is one, may start (every other waits for this grid's end)
+  if ((int)blockIdx.x >= ncta) {
+    zero_fill(fill, fill_bytes, blockIdx.x - ncta, gridDim.x - ncta);
+    return;
+  }
+  int2 *moved = reinterpret_cast<int2 *>(sh);                    // [TILE] key, row of the positions held
+  int *total = sh + 2 * TILE;                                    // [bins] points of each digit here
+  int *dbase = total + bins;                                     // [bins] where this CTA's points of a digit go
+  int *wsum = dbase + bins;                                      // [kFewWarps]
+  unsigned *wmask = reinterpret_cast<unsigned *>(wsum + kFewWarps);  // [kFewWarps][bins]
+  int *wcnt = reinterpret_cast<int *>(wmask) + kFewWarps * bins;     // [kFewWarps][bins + 1]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = blockIdx.x, stride = bins + 1;
+  const int here = warp * (32 * ITEMS) + lane;  // of the thread's first item
+  const int base = rank * TILE + here;
+  int key[ITEMS], val[ITEMS], place[ITEMS];
+  bool bad = false;
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it) {
+    const int pos = base + it * 32;
+    val[it] = pos;
+    key[it] = pos < rows ? labels[pos] : 0;
+  }
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it)
+    if (base + it * 32 < rows) key[it] = key_of_label<true>(key[it], base + it * 32, N, K, B, bad);
+  if (bad) record_status(status, kStBadLabel);
+  int *mycnt = wcnt + warp * stride;
+  unsigned *mymask = wmask + warp * bins;
+  for (int pass = 0; pass < npass; ++pass) {
+    const int shift = pass * bits;
+    for (int i = tid; i < kFewWarps * stride; i += kFewThreads) wcnt[i] = 0;
+    for (int i = tid; i < kFewWarps * bins; i += kFewThreads) wmask[i] = 0u;
+    __syncthreads();
+    // stable ranks within each warp's consecutive positions, as in radix_scatter_kernel
+    unsigned peer[ITEMS];
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const bool valid = base + it * 32 < rows;
+      const int d = key[it] >> shift & (bins - 1);
+      if (valid) atomicOr(mymask + d, 1u << lane);
+      __syncwarp();
+      const unsigned peers = valid ? mymask[d] : 0u;
+      __syncwarp();
+      int c = 0;
+      if (valid && lane == __ffs(peers) - 1) {
+        mymask[d] = 0u;
+        c = atomicAdd(mycnt + d, __popc(peers));
+      }
+      __syncwarp();
+      peer[it] = peers;
+      place[it] = c;
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it)
+      place[it] = __shfl_sync(0xffffffffu, place[it], (__ffs(peer[it]) - 1) & 31) + __popc(peer[it] & ((1u << lane) - 1u));
+    __syncthreads();
+    if (tid < bins) {  // per digit: exclusive prefix over the warps, and the CTA's count
+      int r = 0;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const int t = wcnt[w * stride + tid];
+        wcnt[w * stride + tid] = r;
+        r += t;
+      }
+      total[tid] = r;
+    }
+    cluster_sync();  // every CTA has its counts, and has read the points it held
+    int all = 0, before = 0;
+    if (tid < bins)
+#pragma unroll
+      for (int c = 0; c < kFewCtas; ++c)
+        if (c < ncta) {
+          const int t = (int)ld_cluster(map_to_cta(smem_u32(&total[tid]), c));
+          all += t;
+          if (c < rank) before += t;
+        }
+    int incl = all;  // over the digits
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int run = incl - all + before;
+    for (int w = 0; w < warp; ++w) run += wsum[w];
+    if (tid < bins) dbase[tid] = run;
+    __syncthreads();
+    const bool last = pass == npass - 1;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it)
+      if (base + it * 32 < rows) {
+        const int d = key[it] >> shift & (bins - 1);
+        const int to = dbase[d] + mycnt[d] + place[it];
+        if (last) {
+          skeys[to] = key[it];
+          perm[to] = val[it];
+        } else {
+          st_cluster2(map_to_cta(smem_u32(&moved[to % TILE]), to / TILE), key[it], val[it]);
+        }
+      }
+    cluster_sync();  // the points have moved, and no CTA reads the others' counts any more
+    if (!last)
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        const int2 p = moved[here + it * 32];
+        key[it] = p.x;
+        val[it] = p.y;
+      }
+  }
+}
+
+// Zero-fills beside the sort that was launched before it: it starts when the
+// sort has (so everything before the sort is done), and ends when the sort
+// has, so that what waits for it has waited for both.
+__global__ void __launch_bounds__(512) fill_kernel(char *fill, size_t bytes) {
+  zero_fill(fill, bytes, blockIdx.x, gridDim.x);
+  wait_prior_grid();
+}
+
+static cudaError_t run_sort_few(const int32_t *labels, int B, int N, int K, void *ws, int *status, cudaStream_t s,
+                                LabelSort *out, void *fill, size_t fill_bytes) {
+  const int rows = B * N;
+  const long long Ktot = (long long)B * K;
+  int keybits = ceil_log2(Ktot + 1);
+  if (keybits < 1) keybits = 1;
+  const int npass = (keybits + kFewBits - 1) / kFewBits, bits = (keybits + npass - 1) / npass, bins = 1 << bits;
+  // four points a thread and more CTAs before more points a thread
+  int ncta = 1, items = 2;
+  if (rows > kFewThreads * items) items = 4;
+  while (ncta < kFewCtas && rows > kFewThreads * items * ncta) ncta *= 2;
+  while (rows > kFewThreads * items * ncta) items *= 2;
+  const auto kernel = items == 2 ? sort_few_kernel<2>
+                      : items == 4 ? sort_few_kernel<4> : sort_few_kernel<8>;
+  {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !configured[dev]) {
+      const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+      cudaError_t e = cudaFuncSetAttribute(sort_few_kernel<2>, at, few_smem_bytes(kFewBins, 2));
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(sort_few_kernel<4>, at, few_smem_bytes(kFewBins, 4));
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(sort_few_kernel<8>, at, few_smem_bytes(kFewBins, 8));
+      if (e != cudaSuccess) return e;
+      configured[dev] = true;
+    }
+  }
+  // beside the sort: one block of 512 threads an SM, with 32 KB to fill at
+  // least.  They write 4 TB/s where a kernel of its own writes 7 (16,384 x
+  // 2,048 bf16 into 131,072 rows, 537 MB: 159 us against 114), but need no
+  // launch: up to kFewFill bytes, what the sort itself takes
+  const bool apart = fill_bytes > kFewFill;
+  long long fillers = apart ? 0 : (long long)((fill_bytes + 32767) / 32768);
+  if (fillers > 148) fillers = 148;
+  fillers = (fillers + ncta - 1) / ncta * ncta;
+  int32_t *keys = (int32_t *)ws, *ids = (int32_t *)((char *)ws + al256((size_t)rows * 4));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ncta + (unsigned)fillers);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = few_smem_bytes(bins, items);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ncta;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, labels, rows, N, K, B, npass, bits, bins, keys, ids, (char *)fill,
+                                     fill_bytes, ncta, status);
+  count_launches(1);
+  if (e == cudaSuccess && apart) {
+    const size_t blocks = fill_bytes / (512 * 16 * 8) + 1;  // eight vectors a thread
+    e = launch_chained(fill_kernel, dim3((unsigned)(blocks < (1u << 20) ? blocks : 1u << 20)), dim3(512), 0, s,
+                       (char *)fill, fill_bytes);
+    count_launches(1);
+  }
+  out->skeys = keys;
+  out->perm = ids;
+  return e;
+}
+
+// ---------------------------------------------------------------- host ---
 
 struct SortWs {
   int32_t *kA, *vA, *kB, *vB;
@@ -419,10 +659,19 @@ static cudaError_t run_sort(const int32_t *labels, int B, int N, int K, void *ws
   return cudaGetLastError();
 }
 
-cudaError_t launch_label_sort(const int32_t *labels, int B, int N, int K, bool drop, void *ws, int *status,
-                              cudaStream_t s, LabelSort *out) {
-  return drop ? run_sort<true>(labels, B, N, K, ws, status, s, out)
-              : run_sort<false>(labels, B, N, K, ws, status, s, out);
+cudaError_t launch_label_sort(const int32_t *labels, int B, int N, int K, void *ws, int *status, cudaStream_t s,
+                              LabelSort *out) {
+  return run_sort<false>(labels, B, N, K, ws, status, s, out);
+}
+
+cudaError_t launch_label_sort_drop(const int32_t *labels, int B, int N, int K, void *ws, int *status, cudaStream_t s,
+                                   LabelSort *out, void *fill, size_t fill_bytes) {
+  if ((long long)B * N <= kFewPoints) return run_sort_few(labels, B, N, K, ws, status, s, out, fill, fill_bytes);
+  if (fill_bytes > 0) {
+    const cudaError_t e = cudaMemsetAsync(fill, 0, fill_bytes, s);
+    if (e != cudaSuccess) return e;
+  }
+  return run_sort<true>(labels, B, N, K, ws, status, s, out);
 }
 
 }  // namespace fk

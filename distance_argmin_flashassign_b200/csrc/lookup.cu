@@ -242,14 +242,15 @@ cudaError_t launch_lookup(const LookupArgs &a, int *status, cudaStream_t s) {
 }
 
 // --------------------------------------------------------------- gradient --
-// Sorted positions per worker, from the number of 16-byte pieces of dY alone,
+// Sorted positions per worker, eight at least (few rows: 1,000 x 64 bf16 13 us,
+// 20 us with 32 at least), from the number of 16-byte pieces of dY alone,
 // so that the order of a sum depends on the sizes and on nothing else.
 // 148 SMs hold 113,664 lanes of the row-sum kernel (3 blocks of 256).
 static int grad_rows_R(long long rows, int row_bytes) {
   const long long pieces = rows * ((row_bytes + 15) / 16);
   long long R = (pieces + 113663) / 113664;
   R = (R + 7) / 8 * 8;
-  return (int)(R < 32 ? 32 : R > 512 ? 512 : R);
+  return (int)(R < 8 ? 8 : R > 512 ? 512 : R);
 }
 
 __device__ __forceinline__ void add2(float *a, const float *b) {  // two fp32 additions an instruction
@@ -538,13 +539,10 @@ static void launch_grad_from(const LookupGradArgs &a, const LabelSort &o, int ro
 
 cudaError_t launch_lookup_grad(const LookupGradArgs &a, void *ws, int *status, cudaStream_t s) {
   const long long rows = (long long)a.B * a.N, Ktot = (long long)a.B * a.K;
-  if (!a.accumulate) {
-    cudaError_t e = cudaMemsetAsync(a.dT, 0, (size_t)Ktot * a.D * dtype_size(a.dt_t), s);
-    if (e != cudaSuccess) return e;
-  }
-  if (rows == 0) return cudaSuccess;
+  const size_t fill = a.accumulate ? 0 : (size_t)Ktot * a.D * dtype_size(a.dt_t);  // rows without a label
+  if (rows == 0) return fill > 0 ? cudaMemsetAsync(a.dT, 0, fill, s) : cudaSuccess;
   LabelSort o;
-  cudaError_t e = launch_label_sort(a.ids, a.B, a.N, a.K, true, ws, status, s, &o);
+  cudaError_t e = launch_label_sort_drop(a.ids, a.B, a.N, a.K, ws, status, s, &o, a.dT, fill);
   if (e != cudaSuccess) return e;
   float *parts = (float *)((char *)ws + al256(label_sort_bytes(rows, Ktot, a.B, true)));
   const int R = grad_rows_R(rows, a.D * (int)dtype_size(a.dt)), none = (int)Ktot, n = (int)rows;

@@ -713,7 +713,7 @@ cudaError_t launch_update(const UpdateArgs &a, void *ws, size_t ws_bytes, DevCtl
   if (w.bytes > ws_bytes) return cudaErrorInvalidValue;
   const int N = (int)Ntot;
   LabelSort order;
-  cudaError_t e = launch_label_sort(a.labels, a.B, a.N, a.K, false, w.sort, ctl.status, s, &order);
+  cudaError_t e = launch_label_sort(a.labels, a.B, a.N, a.K, w.sort, ctl.status, s, &order);
   if (e != cudaSuccess) return e;
   const int32_t *skeys = order.skeys, *perm = order.perm;
   const int R = chunk_rows_R(Ntot);
