@@ -59,6 +59,11 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+__device__ __forceinline__ float warp_max(float v) {  // ignores NaN
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     // every team a row: probabilities into the column sums, maximum and sum kept
     for (int s0 = 0; s0 < n; s0 += U * t.rows) {
       L x[U];
-      float m[U], s[U], sum[U];
+      float own[U], m[U], s[U], sum[U];
       float2 z[U][NP];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -438,18 +443,16 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
         const T *row = zs + r * E;
 #pragma unroll
         for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, live && (p * G + t.lane) * VL < E);
-        m[u] = x[u].max();
+        own[u] = m[u] = x[u].max();
       }
-#pragma unroll
-      for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+      // each lane's exponentials are of its own maximum, so that they need not
+      // wait for the team's; a lane or team without a logit above -inf takes 0
+      // for its maximum: its sum is 0 (or NaN)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        // a team without a logit above -inf takes 0 for its maximum: its sum is 0 (or NaN)
-        if (m[u] == neg_inf()) m[u] = 0.f;
+        if (own[u] == neg_inf()) own[u] = 0.f;
         x[u].values(z[u]);
-        float top = m[u];
+        float top = own[u];
         if (!kIsHalf<T> && fabsf(top) > 1e38f) {  // its product with log2(e) would overflow (the type's lowest values)
 #pragma unroll
           for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
@@ -466,12 +469,28 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
         }
         s[u] = ss.x + ss.y;
       }
+      if constexpr (WIDE || LOGG == 5) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) m[u] = warp_max(m[u]);
+      } else {
+#pragma unroll
+        for (int o = G >> 1; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+      }
+      float w[U];  // exp(own - m): the lane's sum and probabilities on the team's scale
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (m[u] == neg_inf()) m[u] = 0.f;
+        w[u] = s[u] == 0.f ? 0.f : exp2_fast((own[u] - m[u]) * kLog2e);
+        s[u] *= w[u];
+      }
 #pragma unroll
       for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
 #pragma unroll
         for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
       if (WIDE) {
-        // z holds exp(z - the warp's maximum): one exchange of the warps' maxima and sums
+        // one exchange of the warps' maxima and sums
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
           for (int u = 0; u < U; ++u) {
@@ -483,18 +502,17 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = s0 + u * t.rows + t.row0;
-        float factor;  // p_e = z_e factor
+        float factor;  // p_e = z_e w factor
         if (WIDE) {
-          float top = neg_inf();
-          sum[u] = 0.f;
+          // lane l looks at warp l % 8
+          const float mw = wm[buf][u][threadIdx.x % kBalWarps], sw = wsum[buf][u][threadIdx.x % kBalWarps];
+          float top = mw;
 #pragma unroll
-          for (int w = 0; w < kBalWarps; ++w) top = fmaxf(top, wm[buf][u][w]);
+          for (int o = kBalWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (top == neg_inf()) top = 0.f;
+          sum[u] = sw == 0.f ? 0.f : sw * exp2_fast((mw - top) * kLog2e);
 #pragma unroll
-          for (int w = 0; w < kBalWarps; ++w) {
-            const float v = wsum[buf][u][w];
-            sum[u] += v * (v == 0.f ? 0.f : exp2_fast((wm[buf][u][w] - top) * kLog2e));
-          }
+          for (int o = kBalWarps / 2; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
           // NaN in every warp of a NaN row, 0 in every warp of a row left out
           factor = sum[u] == 0.f ? 0.f : (s[u] == 0.f ? 0.f : exp2_fast((m[u] - top) * kLog2e)) * rcp_fast(sum[u]);
           m[u] = top;
@@ -503,7 +521,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
           factor = sum[u] == 0.f ? 0.f : rcp_fast(sum[u]);
         }
 #pragma unroll
-        for (int i = 0; i < NP; ++i) acc[i] = fma2(z[u][i], both(factor), acc[i]);
+        for (int i = 0; i < NP; ++i) acc[i] = fma2(z[u][i], both(w[u] * factor), acc[i]);
         if (t.lane == 0 && r < n) stat[in_batch + r] = make_float2(m[u], sum[u]);
       }
       buf ^= 1;
