@@ -440,7 +440,7 @@ def fk_balance(Z, ids, mask=None, coef=1.0, loss=None, counts=None, tokens=None,
     B, N, E, bat = _dims(Z)
     lead, top = ((B, N), (B,)) if bat else ((N,), ())
     dt, dev = _dtype(Z), Z.device
-    M = 1 if ids.dim() == len(lead) else ids.shape[-1]
+    M = 1 if ids.dim() == len(lead) or ids.dim() == 0 else ids.shape[-1]
     _need(Z, "Z", Z.dtype, Z.shape, dev)
     _need(ids, "ids", torch.int32, lead if ids.dim() == len(lead) else lead + (M,), dev)
     if mask is not None:

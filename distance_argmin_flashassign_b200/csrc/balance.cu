@@ -7,12 +7,23 @@
 //   P_e = (1/n) sum_i p_ie         f_e = count_e / (M n)
 //   loss = coef E sum_e f_e P_e
 //   dz_ie = g coef E / n  p_ie (f_e - sum_j f_j p_ij)
-// One pass over the logits forward, one backward: a row lives in the
-// registers of a team of lanes, its probabilities are added to the column
-// sums that each lane keeps in registers over all of its rows, and blocks
-// leave their sums in partial rows that a second kernel adds in block order.
-// Counts are integers, so the shared-memory atomics that make them do not
-// change the result.
+// One pass over the logits forward, one backward.  A row belongs to a team of
+// lanes that hold its columns in registers; a warp (for long rows the block)
+// is the owner of a run of rows, whose logits come to it through a ring of
+// tiles in shared memory.  Forward, a team adds its rows' probabilities to
+// column sums that its lanes keep in registers over all of their rows; blocks
+// leave their sums in partial rows that a second small kernel adds in block
+// order.  Counts are integers, so the shared-memory atomics that make them do
+// not change the result.
+//
+// What bounds it (B200, HBM copy rate 6,466 GB/s): backward HBM, 0.80 of the
+// copy rate from 64 to 8,192 columns (16 x 32,768 x 64 bf16 27.6 us, 1 M x 128
+// 105 us).  Forward issue slots: a bf16 logit takes 8 to 12 instructions with
+// its share of the row's and the tile's, of which the special-function unit
+// serves one (29 us of the 81 us of 1 M x 128 bf16); fp32 rows, half as many
+// logits a byte, reach 0.74 of the copy rate, bf16 rows 0.42 to 0.55.
+// 262,144 x 1,024 fp16: 131 us, 0.64.  Pairs of fp32 operations in one
+// instruction are worth 5 % of it.
 #include <atomic>
 #include <type_traits>
 
@@ -173,18 +184,14 @@ constexpr int kBalLane = 32, kBalSome = 16;  // columns a lane holds at most, an
 constexpr int kWide = 8;      // the whole block
 constexpr int kAnyTeam = -1;  // up to a warp, known at run time
 
-#ifndef BB8
-#define BB8 3
-#define BB16 2
-#define BU8 2
-#define BU16 2
-#endif
-// Blocks that fit an SM next to a lane's columns in registers.
-constexpr int bal_blocks(int NE) { return NE <= 8 ? BB8 : BB16; }
+// Blocks that fit an SM next to a lane's columns in registers (three with 16
+// or more columns a lane spill: 1 M x 128 bf16 100 us against 81 with two, 131,072 x
+// 1,024 112 against 82).
+constexpr int bal_blocks(int NE) { return NE <= 8 ? 3 : 2; }
 template <int NE> constexpr int kBalBlocks = bal_blocks(NE);
 // Rows a team works on at a time, so that one row's exchanges between lanes
-// are not waited for alone.
-constexpr int bal_rows(int NE) { return NE <= 8 ? BU8 : NE <= 16 ? BU16 : 1; }
+// are not waited for alone (1 M x 128 bf16: 81 us, 89 with one).
+constexpr int bal_rows(int NE) { return NE <= 16 ? 2 : 1; }
 template <int NE> constexpr int kBalRows = bal_rows(NE);
 
 // Rows go tile by tile to owners: a warp, whose G = 2^logg-lane teams take
@@ -209,17 +216,21 @@ template <bool WIDE> struct Owner {
   }
   // sync, and whether any of the owner's threads says so
   __device__ __forceinline__ bool any(bool v) const {
-    return WIDE ? __syncthreads_or(v) != 0 : __any_sync(0xffffffffu, v) != 0;
+    if (WIDE) return __syncthreads_or(v) != 0;
+    __syncwarp();
+    return __any_sync(0xffffffffu, v) != 0;
   }
 };
 
 // ------------------------------------------------------------ row tiles ---
 // Rows are consecutive in memory, so a tile of them is one range of bytes of
-// each array.  One thread of an owner copies the ranges of a tile into a stage
-// of shared memory with bulk copies, a few tiles ahead of the owner's work.  A bulk copy
-// moves whole aligned 16-byte pieces: a range is widened to them (its data
-// then starts (address mod 16) bytes into its place), except at the very ends
-// of the array, where what the pieces inside it leave is copied byte by byte.
+// each array.  One thread of an owner copies the ranges of a tile into its place
+// in shared memory with bulk copies, a few tiles ahead of the owner's work: no
+// registers wait for memory, and rows of any length and alignment arrive at the
+// full rate.  A bulk copy moves whole aligned 16-byte pieces: a range is widened
+// to them (its data then starts (address mod 16) bytes into its place), except
+// at the very ends of the array, where what the pieces inside it leave is
+// copied byte by byte.
 struct Span {
   const char *lo;  // the whole pieces
   uint32_t bytes;
@@ -321,7 +332,8 @@ template <bool WIDE> struct Rows {
   // After a wait that ran out at batch kb, tile kt: let the copies in flight
   // land, within a second each.
   __device__ __forceinline__ void drain(int kb, int kt) const {
-    for (int i = kb; i < kb + 2 && i < nbatches; ++i) mbar_wait_for(smem_u32(&bar->side[i & 1]), i >> 1 & 1, 1000000000ull);
+    for (int i = kb; i < kb + 2 && i < nbatches; ++i)
+      mbar_wait_for(smem_u32(&bar->side[i & 1]), i >> 1 & 1, 1000000000ull);
     for (int i = kt; i < kt + pl.stages && i < ntiles; ++i)
       mbar_wait_for(smem_u32(&bar->tile[i % pl.stages]), i / pl.stages & 1, 1000000000ull);
   }
@@ -428,111 +440,111 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     const int *cs = reinterpret_cast<const int *>(v.mid_at(kb & 1) + v.skew(v.mid, v.midrow, rb));
     const uint8_t *ms = reinterpret_cast<const uint8_t *>(v.small_at(kb & 1) + v.skew(v.small, 1, rb));
     for (int in_batch = 0; in_batch < nrows; in_batch += pl.rows, ++kt) {
-    mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
-    const int n = v.tile_rows(kt);
-    const T *zs = reinterpret_cast<const T *>(v.tile_at(at) + v.skew(v.Z, v.zrow, v.first + (size_t)(kt * pl.rows)));
-    // every team a row: probabilities into the column sums, maximum and sum kept
-    for (int s0 = 0; s0 < n; s0 += U * t.rows) {
-      L x[U];
-      float own[U], m[U], s[U], sum[U];
-      float2 z[U][NP];
+      mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
+      const int n = v.tile_rows(kt);
+      const T *zs = reinterpret_cast<const T *>(v.tile_at(at) + v.skew(v.Z, v.zrow, v.first + (size_t)(kt * pl.rows)));
+      // every team a row: probabilities into the column sums, maximum and sum kept
+      for (int s0 = 0; s0 < n; s0 += U * t.rows) {
+        L x[U];
+        float own[U], m[U], s[U], sum[U];
+        float2 z[U][NP];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = s0 + u * t.rows + t.row0;
-        const bool live = r < n && (!mask || ms[in_batch + r] != 0);
-        const T *row = zs + r * E;
+        for (int u = 0; u < U; ++u) {
+          const int r = s0 + u * t.rows + t.row0;
+          const bool live = r < n && (!mask || ms[in_batch + r] != 0);
+          const T *row = zs + r * E;
 #pragma unroll
-        for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, live && (p * G + t.lane) * VL < E);
-        own[u] = m[u] = x[u].max();
-      }
-      // each lane's exponentials are of its own maximum, so that they need not
-      // wait for the team's; a lane or team without a logit above -inf takes 0
-      // for its maximum: its sum is 0 (or NaN)
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (own[u] == neg_inf()) own[u] = 0.f;
-        x[u].values(z[u]);
-        float top = own[u];
-        if (!kIsHalf<T> && fabsf(top) > 1e38f) {  // its product with log2(e) would overflow (the type's lowest values)
-#pragma unroll
-          for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
-          top = 0.f;
+          for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, live && (p * G + t.lane) * VL < E);
+          own[u] = m[u] = x[u].max();
         }
-        float2 ss = both(0.f);
-        const float2 shift = both(-top * kLog2e);
+        // each lane's exponentials are of its own maximum, so that they need not
+        // wait for the team's; a lane or team without a logit above -inf takes 0
+        // for its maximum: its sum is 0 (or NaN)
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          z[u][i] = fma2(z[u][i], both(kLog2e), shift);
-          z[u][i].x = exp2_fast(z[u][i].x);
-          z[u][i].y = exp2_fast(z[u][i].y);
-          ss = add2(ss, z[u][i]);
-        }
-        s[u] = ss.x + ss.y;
-      }
-      if constexpr (WIDE || LOGG == 5) {
+        for (int u = 0; u < U; ++u) {
+          if (own[u] == neg_inf()) own[u] = 0.f;
+          x[u].values(z[u]);
+          float top = own[u];
+          if (!kIsHalf<T> && fabsf(top) > 1e38f) {  // its product with log2(e) would overflow (the type's lowest values)
 #pragma unroll
-        for (int u = 0; u < U; ++u) m[u] = warp_max(m[u]);
-      } else {
-#pragma unroll
-        for (int o = G >> 1; o > 0; o >>= 1)
-#pragma unroll
-          for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
-      }
-      float w[U];  // exp(own - m): the lane's sum and probabilities on the team's scale
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (m[u] == neg_inf()) m[u] = 0.f;
-        w[u] = s[u] == 0.f ? 0.f : exp2_fast((own[u] - m[u]) * kLog2e);
-        s[u] *= w[u];
-      }
-#pragma unroll
-      for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-      if (WIDE) {
-        // one exchange of the warps' maxima and sums
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            wm[buf][u][threadIdx.x >> 5] = s[u] == 0.f ? neg_inf() : m[u];
-            wsum[buf][u][threadIdx.x >> 5] = s[u];
+            for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
+            top = 0.f;
           }
-        __syncthreads();
-      }
+          float2 ss = both(0.f);
+          const float2 shift = both(-top * kLog2e);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = s0 + u * t.rows + t.row0;
-        float factor;  // p_e = z_e w factor
-        if (WIDE) {
-          // lane l looks at warp l % 8
-          const float mw = wm[buf][u][threadIdx.x % kBalWarps], sw = wsum[buf][u][threadIdx.x % kBalWarps];
-          float top = mw;
+          for (int i = 0; i < NP; ++i) {
+            z[u][i] = fma2(z[u][i], both(kLog2e), shift);
+            z[u][i].x = exp2_fast(z[u][i].x);
+            z[u][i].y = exp2_fast(z[u][i].y);
+            ss = add2(ss, z[u][i]);
+          }
+          s[u] = ss.x + ss.y;
+        }
+        if constexpr (WIDE || LOGG == 5) {
 #pragma unroll
-          for (int o = kBalWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (top == neg_inf()) top = 0.f;
-          sum[u] = sw == 0.f ? 0.f : sw * exp2_fast((mw - top) * kLog2e);
-#pragma unroll
-          for (int o = kBalWarps / 2; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
-          // NaN in every warp of a NaN row, 0 in every warp of a row left out
-          factor = sum[u] == 0.f ? 0.f : (s[u] == 0.f ? 0.f : exp2_fast((m[u] - top) * kLog2e)) * rcp_fast(sum[u]);
-          m[u] = top;
+          for (int u = 0; u < U; ++u) m[u] = warp_max(m[u]);
         } else {
-          sum[u] = s[u];
-          factor = sum[u] == 0.f ? 0.f : rcp_fast(sum[u]);
+#pragma unroll
+          for (int o = G >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+        }
+        float w[U];  // exp(own - m): the lane's sum and probabilities on the team's scale
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (m[u] == neg_inf()) m[u] = 0.f;
+          w[u] = s[u] == 0.f ? 0.f : exp2_fast((own[u] - m[u]) * kLog2e);
+          s[u] *= w[u];
         }
 #pragma unroll
-        for (int i = 0; i < NP; ++i) acc[i] = fma2(z[u][i], both(w[u] * factor), acc[i]);
-        if (t.lane == 0 && r < n) stat[in_batch + r] = make_float2(m[u], sum[u]);
+        for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+        if (WIDE) {
+          // one exchange of the warps' maxima and sums
+          if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              wm[buf][u][threadIdx.x >> 5] = s[u] == 0.f ? neg_inf() : m[u];
+              wsum[buf][u][threadIdx.x >> 5] = s[u];
+            }
+          __syncthreads();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = s0 + u * t.rows + t.row0;
+          float factor;  // p_e = z_e w factor
+          if (WIDE) {
+            // lane l looks at warp l % 8
+            const float mw = wm[buf][u][threadIdx.x % kBalWarps], sw = wsum[buf][u][threadIdx.x % kBalWarps];
+            float top = mw;
+#pragma unroll
+            for (int o = kBalWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (top == neg_inf()) top = 0.f;
+            sum[u] = sw == 0.f ? 0.f : sw * exp2_fast((mw - top) * kLog2e);
+#pragma unroll
+            for (int o = kBalWarps / 2; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+            // NaN in every warp of a NaN row, 0 in every warp of a row left out
+            factor = sum[u] == 0.f ? 0.f : (s[u] == 0.f ? 0.f : exp2_fast((m[u] - top) * kLog2e)) * rcp_fast(sum[u]);
+            m[u] = top;
+          } else {
+            sum[u] = s[u];
+            factor = sum[u] == 0.f ? 0.f : rcp_fast(sum[u]);
+          }
+#pragma unroll
+          for (int i = 0; i < NP; ++i) acc[i] = fma2(z[u][i], both(w[u] * factor), acc[i]);
+          if (t.lane == 0 && r < n) stat[in_batch + r] = make_float2(m[u], sum[u]);
+        }
+        buf ^= 1;
       }
-      buf ^= 1;
-    }
-    gave_up = t.any(*(volatile int *)&abort_flag);  // the tile has been read
-    if (gave_up) break;
-    if (t.thread == 0 && kt + pl.stages < v.ntiles) v.issue_tile(kt + pl.stages, at);
-    if (++at == pl.stages) {
-      at = 0;
-      phase ^= 1;
-    }
+      gave_up = t.any(*(volatile int *)&abort_flag);  // the tile has been read
+      if (gave_up) break;
+      if (t.thread == 0 && kt + pl.stages < v.ntiles) v.issue_tile(kt + pl.stages, at);
+      if (++at == pl.stages) {
+        at = 0;
+        phase ^= 1;
+      }
     }
     if (gave_up) break;
     // every thread a row: what is done once for each
@@ -716,78 +728,78 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     const int nrows = v.batch_rows(kb);
     const float *ls = reinterpret_cast<const float *>(v.mid_at(kb & 1) + v.skew(v.mid, 4, rb));
     for (int in_batch = 0; in_batch < nrows; in_batch += pl.rows, ++kt) {
-    mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
-    const int n = v.tile_rows(kt);
-    const size_t r0 = rb + in_batch;
-    const T *zs = reinterpret_cast<const T *>(v.tile_at(at) + v.skew(v.Z, v.zrow, r0));
-    for (int s0 = 0; s0 < n; s0 += U * t.rows) {
-      L x[U];
-      float2 z[U][NP];
-      float l[U], dot[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = s0 + u * t.rows + t.row0;
-        l[u] = r < n ? ls[in_batch + r] : inf;
-        const T *row = zs + r * E;
-#pragma unroll
-        for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, l[u] != inf && (p * G + t.lane) * VL < E);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        x[u].values(z[u]);
-        float top = l[u];
-        if (!kIsHalf<T> && fabsf(top) > 1e38f && top != inf) {  // as in the forward pass
-#pragma unroll
-          for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
-          top = 0.f;
-        }
-        float2 dd = both(0.f);
-        const float2 shift = both(-top * kLog2e);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          z[u][i] = fma2(z[u][i], both(kLog2e), shift);  // past E -inf: a probability of 0
-          z[u][i].x = exp2_fast(z[u][i].x);
-          z[u][i].y = exp2_fast(z[u][i].y);
-          dd = fma2(kf[i], z[u][i], dd);
-        }
-        dot[u] = dd.x + dd.y;
-      }
-#pragma unroll
-      for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-      if (WIDE) {
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-          for (int u = 0; u < U; ++u) wdot[buf][u][threadIdx.x >> 5] = dot[u];
-        __syncthreads();
+      mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
+      const int n = v.tile_rows(kt);
+      const size_t r0 = rb + in_batch;
+      const T *zs = reinterpret_cast<const T *>(v.tile_at(at) + v.skew(v.Z, v.zrow, r0));
+      for (int s0 = 0; s0 < n; s0 += U * t.rows) {
+        L x[U];
+        float2 z[U][NP];
+        float l[U], dot[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          dot[u] = 0.f;
+          const int r = s0 + u * t.rows + t.row0;
+          l[u] = r < n ? ls[in_batch + r] : inf;
+          const T *row = zs + r * E;
 #pragma unroll
-          for (int w = 0; w < kBalWarps; ++w) dot[u] += wdot[buf][u][w];
+          for (int p = 0; p < P; ++p) x[u].load(p, row, (p * G + t.lane) * VL, l[u] != inf && (p * G + t.lane) * VL < E);
         }
-        buf ^= 1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          x[u].values(z[u]);
+          float top = l[u];
+          if (!kIsHalf<T> && fabsf(top) > 1e38f && top != inf) {  // as in the forward pass
+#pragma unroll
+            for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
+            top = 0.f;
+          }
+          float2 dd = both(0.f);
+          const float2 shift = both(-top * kLog2e);
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            z[u][i] = fma2(z[u][i], both(kLog2e), shift);  // past E -inf: a probability of 0
+            z[u][i].x = exp2_fast(z[u][i].x);
+            z[u][i].y = exp2_fast(z[u][i].y);
+            dd = fma2(kf[i], z[u][i], dd);
+          }
+          dot[u] = dd.x + dd.y;
+        }
+#pragma unroll
+        for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+        if (WIDE) {
+          if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u) wdot[buf][u][threadIdx.x >> 5] = dot[u];
+          __syncthreads();
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            dot[u] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kBalWarps; ++w) dot[u] += wdot[buf][u][w];
+          }
+          buf ^= 1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r = s0 + u * t.rows + t.row0;
+#pragma unroll
+          for (int i = 0; i < NP; ++i) z[u][i] = mul2(z[u][i], add2(kf[i], both(-dot[u])));
+          T *row = dZ + (r0 + r) * E;
+          if (r < n)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              if ((p * G + t.lane) * VL < E) L::store(p, z[u], l[u] == inf, row, (p * G + t.lane) * VL);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = s0 + u * t.rows + t.row0;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) z[u][i] = mul2(z[u][i], add2(kf[i], both(-dot[u])));
-        T *row = dZ + (r0 + r) * E;
-        if (r < n)
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-            if ((p * G + t.lane) * VL < E) L::store(p, z[u], l[u] == inf, row, (p * G + t.lane) * VL);
+      gave_up = t.any(*(volatile int *)&abort_flag);  // the tile has been read, and of a batch's last tile the batch
+      if (gave_up) break;
+      if (t.thread == 0 && kt + pl.stages < v.ntiles) v.issue_tile(kt + pl.stages, at);
+      if (++at == pl.stages) {
+        at = 0;
+        phase ^= 1;
       }
-    }
-    gave_up = t.any(*(volatile int *)&abort_flag);  // the tile has been read, and of a batch's last tile the batch
-    if (gave_up) break;
-    if (t.thread == 0 && kt + pl.stages < v.ntiles) v.issue_tile(kt + pl.stages, at);
-    if (++at == pl.stages) {
-      at = 0;
-      phase ^= 1;
-    }
     }
     if (gave_up) break;
     if (t.thread == 0 && kb + 2 < v.nbatches) v.issue_batch(kb + 2, kb & 1);
@@ -880,7 +892,8 @@ static Grid grid_of(int B, int64_t N, int E, DType dt, int mid, int extra, const
 
 static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 static size_t parts_bytes(int B, int64_t N, int E, DType dt, bool aligned) {
-  const size_t parts = (size_t)B * grid_of(B, N, E, dt, 4, place_of_columns(E), spread_of(E, dt, aligned)).blocks;  // for any M
+  // the blocks do not depend on M
+  const size_t parts = (size_t)B * grid_of(B, N, E, dt, 4, place_of_columns(E), spread_of(E, dt, aligned)).blocks;
   return 2 * al256(parts * E * 4) + al256(parts * 4);
 }
 // Enough for either alignment of Z.
@@ -938,8 +951,8 @@ template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void
     static std::atomic<int> allowed[64];
     e = allow_smem(kernel, g.smem, allowed);
     if (e == cudaSuccess)
-      e = launch_chained(kernel, dim3(nb, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.ids, a.mask, a.B, a.N, a.E,
-                         a.M, p.logg, g.pl, a.lse, psum, csum, tsum, out, ctl);
+      e = launch_chained(kernel, dim3(nb, a.B), dim3(kBalThreads), g.smem, s, (const T *)a.Z, a.ids, a.mask, a.B,
+                         a.N, a.E, a.M, p.logg, g.pl, a.lse, psum, csum, tsum, out, ctl);
   });
   count_launches(1);
   if (e != cudaSuccess || nb == 1) return e;

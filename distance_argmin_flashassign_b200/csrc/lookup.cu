@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(256, 4) lookup_kernel(const TI *__restrict__ T
   };
   auto store = [&](const V *v, long long r32, int j) {
     if (WIDE) {
-      const int r = (int)r32 + j * take + sub;  // below 2^31 + 32: compared unsigned
-      if ((unsigned)r < (unsigned)rows) {
-        TO *p = Yc + (size_t)(unsigned)r * (unsigned)D;
+      const unsigned r = (unsigned)r32 + j * take + sub;  // below 2^31 + 32
+      if (r < (unsigned)rows) {
+        TO *p = Yc + (size_t)r * (unsigned)D;
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (col + u * W * EPL < D) put(v[u], p + u * W * EPL);
