@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 // cluster share a problem's columns and hand their parts of the loss to the
 // first one through its shared memory; in a CTA, groups of threads share a
 // column's partial rows.
-constexpr int kJoinThreads = 512, kJoinCluster = 8;
+constexpr int kJoinThreads = 1024, kJoinCluster = 8;
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const float *__restrict__ psum,
                                                                     const int *__restrict__ csum,
                                                                     const int *__restrict__ tsum, int nparts, int E,

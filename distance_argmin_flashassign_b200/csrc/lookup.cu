@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(1024) grad_join_kernel(const int32_t *__restri
                                                          int D, const float *__restrict__ parts, float scale,
                                                          void *__restrict__ dT, int dt_t, int add) {
   __shared__ float red[32][129];
-  __shared__ int hot_q[32], hot_np[32], nhot;
+  __shared__ int hot_q[32], hot_np[32], hot_k[32], hot_first[32], nhot;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int nchunks = (rows + R - 1) / R, q = blockIdx.x * 32 + w;
   const int c0 = blockIdx.y * kJoinCols, c1 = min(D, c0 + kJoinCols);
@@ -426,19 +426,22 @@ __global__ void __launch_bounds__(1024) grad_join_kernel(const int32_t *__restri
   // following chunks that start with its label (a label's positions are
   // consecutive, so these chunks are too); 1 where it does not start here or
   // does not run past the end
-  int np = 1, k = none;
+  int np = 1, k = none, first = 0;  // first: the chunk's partial row that holds its piece
   if (q < nchunks - 1) {
     const int p0 = q * R, p1 = p0 + R;
     k = skeys[p1 - 1];
     const int after = skeys[p1], before = p0 > 0 ? skeys[p0 - 1] : -1;
+    first = skeys[p0] == k ? 0 : 1;
     if (k != none && after == k && before != k) {
-      // the last such chunk, by 32-fold search: chunk lo starts with k, chunk hi does not
+      // the last such chunk: chunk lo starts with k, chunk hi does not.  32
+      // chunks are looked at first, which is enough for most labels, then 32 of
+      // the rest at equal distances, and so on
       int lo = q + 1, hi = nchunks;
-      while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, i = lo + step * (lane + 1);
+      for (int step = 1; hi - lo > 1; step = (hi - lo + 31) / 32) {
+        const int i = lo + step * (lane + 1);
         const unsigned in = __ballot_sync(0xffffffffu, i < hi && skeys[i < hi ? i * R : 0] == k);
         const int n = __popc(in);
-        hi = min(hi, lo + step * (n + 1));
+        if (n < 32) hi = min(hi, lo + step * (n + 1));
         lo += step * n;
       }
       np = lo - q + 1;
@@ -469,9 +472,10 @@ __global__ void __launch_bounds__(1024) grad_join_kernel(const int32_t *__restri
       const int i = atomicAdd(&nhot, 1);  // any order: each is summed by itself
       hot_q[i] = q;
       hot_np[i] = np;
+      hot_k[i] = k;
+      hot_first[i] = first;
     }
   } else if (np > 1) {
-    const int first = skeys[q * R] == k ? 0 : 1;
     for (int c = c0; c < c1; c += 128) {
       float t[4] = {0.f, 0.f, 0.f, 0.f};
       add_pieces(t, q, first, 0, 1, np, c);
@@ -482,10 +486,10 @@ __global__ void __launch_bounds__(1024) grad_join_kernel(const int32_t *__restri
   }
   __syncthreads();
   for (int h = 0; h < nhot; ++h) {
-    const int hq = hot_q[h], hk = skeys[hq * R + R - 1], first = skeys[hq * R] == hk ? 0 : 1;
+    const int hq = hot_q[h], hk = hot_k[h];
     for (int c = c0; c < c1; c += 128) {
       float t[4] = {0.f, 0.f, 0.f, 0.f};
-      add_pieces(t, hq, first, w, 32, hot_np[h], c);
+      add_pieces(t, hq, hot_first[h], w, 32, hot_np[h], c);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) red[w][lane + 32 * jj] = t[jj];
       __syncthreads();
@@ -550,9 +554,11 @@ cudaError_t launch_lookup_grad(const LookupGradArgs &a, void *ws, int *status, c
   else if (a.dt == kF16) launch_grad_from<__half>(a, o, n, none, R, parts, s);
   else launch_grad_from<__nv_bfloat16>(a, o, n, none, R, parts, s);
   const int nchunks = (n + R - 1) / R;
-  launch_chained(grad_join_kernel, dim3((nchunks + 31) / 32, (a.D + kJoinCols - 1) / kJoinCols), dim3(1024), 0, s, o.skeys, n, none, R, a.D,
-                 parts, a.scale, a.dT, (int)a.dt_t, a.accumulate);
-  count_launches(2);
+  count_launches(1);
+  if (nchunks == 1) return cudaGetLastError();  // no segment runs past a chunk
+  launch_chained(grad_join_kernel, dim3((nchunks + 31) / 32, (a.D + kJoinCols - 1) / kJoinCols), dim3(1024), 0, s,
+                 o.skeys, n, none, R, a.D, parts, a.scale, a.dT, (int)a.dt_t, a.accumulate);
+  count_launches(1);
   return cudaGetLastError();
 }
 
