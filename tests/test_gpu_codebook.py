@@ -574,3 +574,52 @@ def test_the_gradient_sums_are_the_updates():
     assert torch.equal(counts.cpu().double(), cnt[0])
     tol = 2 * (cnt[0] + 3)[:, None] * ref.U * mag[0]
     assert bool(((C.double() * counts[:, None]).cpu() - S.double().cpu()).abs().le(tol).all())
+
+
+def test_as_many_problems_as_there_may_be():
+    """B = 65,535 problems of a few rows each."""
+    B, N, K, D = 65535, 3, 2, 4
+    T = torch.randn(B, K, D, generator=gen(60)).half()
+    ids = labels((B, N), K, 61)
+    Y = fk.fk_lookup(T.to(DEV), ids.to(DEV))
+    assert torch.equal(Y.cpu().double(), ref.lookup(T, ids, 1.0))
+    dT = fk.fk_lookup_grad(Y, ids.to(DEV), K)
+    g, mag, cnt = ref.lookup_grad(Y.cpu(), ids, K, 1.0)
+    assert bool(((dT.cpu().double() - g).abs() <= ref.lookup_grad_tol(g, mag, cnt, torch.float32)).all())
+    Z = torch.randn(B, N, 4, generator=gen(62))
+    ch = torch.randint(-1, 4, (B, N, 2), generator=gen(63), dtype=torch.int32)
+    Zd, out = _call_bal(Z, ch, None, 0, 1.0)
+    r = ref.balance(Z, ch, None, 1.0)
+    _check_bal(out, Z, r)
+    dZ = fk.fk_balance_grad(Zd, out["counts"], out["tokens"], out["lse"], 2)
+    one = torch.ones(B)
+    err = (dZ.double().cpu() - ref.balance_grad(r, one, 1.0)).abs()
+    assert bool((err <= ref.balance_grad_tol(Z, r, one, 1.0, torch.float32)).all())
+
+
+@pytest.mark.parametrize("N", [32768, 32769, 100000])
+def test_lookup_grad_either_side_of_the_one_launch_sort(N):
+    """The same labels and rows, sorted by one cluster (up to 32,768 rows) and by
+    the kernels for more: rows behind the first 32,768 carry no label."""
+    K, D = 5000, 32
+    dY = torch.randn(N, D, generator=gen(70)).half()
+    ids = labels((N,), K, 71, hot=0.1)
+    ids[32768:] = -1
+    a = fk.fk_lookup_grad(dY.to(DEV), ids.to(DEV), K)
+    b = fk.fk_lookup_grad(dY[:32768].to(DEV).contiguous(), ids[:32768].to(DEV).contiguous(), K)
+    _, mag, cnt = ref.lookup_grad(dY[None], ids[None], K, 1.0)
+    # two orders of the same sums
+    assert bool(((a.double() - b.double()).abs().cpu() <= 2 * (cnt[0][:, None] + 2) * ref.U * mag[0]).all())
+
+
+@pytest.mark.parametrize("K", [1, 2, 510, 511, 512, 262142, 262143, 262144, (1 << 22) - 1])
+def test_lookup_grad_at_the_digits_edges(K):
+    """Key counts around the sorts' digit and pass borders, the largest labels among them."""
+    N, D = 3000, 2
+    dY = torch.randn(N, D, generator=gen(80))
+    ids = labels((N,), K, 81)
+    ids[:3] = K - 1
+    dT = fk.fk_lookup_grad(dY.to(DEV), ids.to(DEV), K).cpu()
+    fk.fk_sync()
+    g, mag, cnt = ref.lookup_grad(dY[None], ids[None], K, 1.0)
+    assert bool(((dT.double() - g[0]).abs() <= ref.lookup_grad_tol(g, mag, cnt, torch.float32)[0]).all())
