@@ -101,33 +101,40 @@ template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t a, uint3
   return w;
 }
 
-// The columns a lane holds of one row: P packs of VL consecutive elements
-// (a whole 16 bytes, or a single element), as they lie in memory.  A row of
-// which nothing is looked at, and columns past E, count as -inf.
+// The columns a lane holds of one row: P packs of VL consecutive elements (a
+// whole 16 bytes, two of 16 bits, or a single element), as they lie in memory.
+// A row of which nothing is looked at, and columns past E, count as -inf.
 template <typename T, int VL, int P> struct Lane {
   static constexpr int NE = VL * P, NP = (NE + 1) / 2;  // columns, pairs of them
   static constexpr bool kWords = VL > 1 && sizeof(T) == 2;
-  uint4 w[VL > 1 ? P : 1];
+  static constexpr int W = VL * (int)sizeof(T) / 4;  // 32-bit words of a pack
+  uint32_t w[VL > 1 ? P * W : 1];
   float e[VL > 1 ? 1 : P];
   // p-th pack from column c of `row` in shared memory
   __device__ __forceinline__ void load(int p, const T *row, int c, bool ok) {
     if constexpr (VL == 1) {
       e[p] = ok ? to_f32<T>(row[c]) : neg_inf();
     } else {
-      const unsigned n = sizeof(T) == 4 ? 0xff800000u : kIsHalf<T> ? 0xfc00fc00u : 0xff80ff80u;
-      w[p] = make_uint4(n, n, n, n);
-      if (ok) w[p] = *reinterpret_cast<const uint4 *>(row + c);
+      const uint32_t n = sizeof(T) == 4 ? 0xff800000u : kIsHalf<T> ? 0xfc00fc00u : 0xff80ff80u;
+      if constexpr (W == 4) {
+        uint4 v = make_uint4(n, n, n, n);
+        if (ok) v = *reinterpret_cast<const uint4 *>(row + c);
+        w[4 * p] = v.x;
+        w[4 * p + 1] = v.y;
+        w[4 * p + 2] = v.z;
+        w[4 * p + 3] = v.w;
+      } else {
+        static_assert(W == 1, "whole 16-byte packs or pairs of 16 bits");
+        w[p] = ok ? *reinterpret_cast<const uint32_t *>(row + c) : n;
+      }
     }
   }
   __device__ __forceinline__ float max() const {
     float m = neg_inf();
     if constexpr (kWords) {
-      uint32_t t = w[0].x;
+      uint32_t t = w[0];
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        if (p > 0) t = max2<T>(t, w[p].x);
-        t = max2<T>(max2<T>(t, w[p].y), max2<T>(w[p].z, w[p].w));
-      }
+      for (int i = 1; i < P * W; ++i) t = max2<T>(t, w[i]);
       const float2 f = unpack2<T>(t);
       m = fmaxf(m, fmaxf(f.x, f.y));
     } else {
@@ -139,23 +146,11 @@ template <typename T, int VL, int P> struct Lane {
     return m;
   }
   __device__ __forceinline__ void values(float2 *z) const {
-    if constexpr (VL == 1) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) z[i] = make_float2(e[2 * i], 2 * i + 1 < P ? e[2 * i + 1] : neg_inf());
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        z[2 * p] = make_float2(__uint_as_float(w[p].x), __uint_as_float(w[p].y));
-        z[2 * p + 1] = make_float2(__uint_as_float(w[p].z), __uint_as_float(w[p].w));
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        z[4 * p] = unpack2<T>(w[p].x);
-        z[4 * p + 1] = unpack2<T>(w[p].y);
-        z[4 * p + 2] = unpack2<T>(w[p].z);
-        z[4 * p + 3] = unpack2<T>(w[p].w);
-      }
+    for (int i = 0; i < NP; ++i) {
+      if constexpr (VL == 1) z[i] = make_float2(e[2 * i], 2 * i + 1 < P ? e[2 * i + 1] : neg_inf());
+      else if constexpr (sizeof(T) == 4) z[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else z[i] = unpack2<T>(w[i]);
     }
   }
   // stores the p-th pack of z, or zeros, from column c of `row`
@@ -163,6 +158,8 @@ template <typename T, int VL, int P> struct Lane {
     if constexpr (VL == 1) {
       const float v = p & 1 ? z[p / 2].y : z[p / 2].x;
       row[c] = from_f32<T>(zero ? 0.f : v);
+    } else if constexpr (W == 1) {
+      *reinterpret_cast<uint32_t *>(row + c) = zero ? 0u : pack2<T>(z[p]);
     } else {
       uint4 o;
       if constexpr (sizeof(T) == 4) {
@@ -809,7 +806,9 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 
 // ---------------------------------------------------------------- host ---
 // How a row of E logits is spread: whole 16-byte packs when the rows and the
-// pointers are whole 16-byte pieces, else single elements; about 16 columns a
+// pointers are whole 16-byte pieces, else pairs of 16-bit elements where they
+// are whole 4-byte pieces (262,144 x 258 bf16: 72 us, element by element 89;
+// backward 83 and 123), else single elements; about 16 columns a
 // lane where that needs no more than a warp, up to kBalLane, and from there on
 // the whole block.  Fewer lanes a row exchange less: with 16 columns a lane in
 // place of 8 ...
@@ -820,10 +819,11 @@ struct Spread {
   int resident;  // blocks an SM
   int owners;    // of a block
 };
-static Spread spread_of(int E, DType dt, bool aligned) {
+static Spread spread_of(int E, DType dt, int aligned) {  // aligned: bytes, of the pointers
   Spread p{};
-  const int full = 16 / (int)dtype_size(dt);
-  p.VL = aligned && E % full == 0 ? full : 1;
+  const int row = E * (int)dtype_size(dt);
+  const int unit = row % 16 == 0 && aligned % 16 == 0 ? 16 : row % 4 == 0 && aligned % 4 == 0 ? 4 : 2;
+  p.VL = unit > (int)dtype_size(dt) ? unit / (int)dtype_size(dt) : 1;
   const int packs = (E + p.VL - 1) / p.VL, most = kBalLane / p.VL, some = kBalSome / p.VL;
   p.wide = packs > 32 * most;
   const int lanes = p.wide ? kBalThreads : 32;
@@ -891,16 +891,21 @@ static Grid grid_of(int B, int64_t N, int E, DType dt, int mid, int extra, const
 }
 
 static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
-static size_t parts_bytes(int B, int64_t N, int E, DType dt, bool aligned) {
+static size_t parts_bytes(int B, int64_t N, int E, DType dt, int aligned) {
   // the blocks do not depend on M
   const size_t parts = (size_t)B * grid_of(B, N, E, dt, 4, place_of_columns(E), spread_of(E, dt, aligned)).blocks;
   return 2 * al256(parts * E * 4) + al256(parts * 4);
 }
-// Enough for either alignment of Z.
+// Enough for any alignment of Z.
 size_t balance_workspace_bytes(int B, int64_t N, int E, DType dt) {
-  const size_t a = parts_bytes(B, N, E, dt, true), u = parts_bytes(B, N, E, dt, false);
-  return a > u ? a : u;
+  size_t most = 0;
+  for (int aligned : {16, 4, 2}) {
+    const size_t n = parts_bytes(B, N, E, dt, aligned);
+    if (n > most) most = n;
+  }
+  return most;
 }
+static int alignment(const void *p) { return (uintptr_t)p % 16 == 0 ? 16 : (uintptr_t)p % 4 == 0 ? 4 : 2; }
 
 // Lets a kernel have `bytes` of dynamic shared memory; `allowed` remembers per
 // device what it may have already.
@@ -929,7 +934,13 @@ template <typename T, typename F> static void with_spread(const Spread &p, F f) 
   if constexpr (H == 2) { FK_P(V, 1, kWide) }
   FK_P(V, 2, kWide) FK_P(V, 4, kWide)
   if constexpr (H == 4) { FK_P(V, 8, kWide) }
-  FK_P(1, 1, 0) FK_P(1, 2, 0) FK_P(1, 4, 0) FK_P(1, 8, 0) FK_P(1, 12, kAnyTeam) FK_P(1, 16, kAnyTeam)
+  if constexpr (V == 8) {
+    FK_P(2, 1, 0) FK_P(2, 2, 0) FK_P(2, 4, 0) FK_P(2, 8, 0) FK_P(2, 8, 1) FK_P(2, 8, 2) FK_P(2, 8, 3) FK_P(2, 8, 4)
+    FK_P(2, 8, 5) FK_P(2, 12, 5) FK_P(2, 16, 5)
+    FK_P(2, 4, kWide) FK_P(2, 8, kWide) FK_P(2, 12, kWide) FK_P(2, 16, kWide)
+  }
+  FK_P(1, 1, 0) FK_P(1, 2, 0) FK_P(1, 4, 0) FK_P(1, 8, 0) FK_P(1, 12, 5) FK_P(1, 16, 5)
+  FK_P(1, 12, kAnyTeam) FK_P(1, 16, kAnyTeam)
   FK_P(1, 20, 5) FK_P(1, 24, 5) FK_P(1, 28, 5) FK_P(1, 32, 5)
   FK_P(1, 8, kWide) FK_P(1, 12, kWide) FK_P(1, 16, kWide) FK_P(1, 20, kWide) FK_P(1, 24, kWide) FK_P(1, 28, kWide)
   FK_P(1, 32, kWide)
@@ -937,7 +948,7 @@ template <typename T, typename F> static void with_spread(const Spread &p, F f) 
 }
 
 template <typename T> static cudaError_t balance_from(const BalanceArgs &a, void *ws, DevCtl ctl, cudaStream_t s) {
-  const Spread p = spread_of(a.E, a.dt, (uintptr_t)a.Z % 16 == 0);
+  const Spread p = spread_of(a.E, a.dt, alignment(a.Z));
   const Grid g = grid_of(a.B, a.N, a.E, a.dt, 4 * a.M, place_of_columns(a.E), p);
   const int nb = g.blocks;
   const size_t parts = (size_t)a.B * nb;
@@ -981,7 +992,7 @@ cudaError_t launch_balance(const BalanceArgs &a, void *ws, DevCtl ctl, cudaStrea
 }
 
 template <typename T> static cudaError_t balance_grad_from(const BalanceGradArgs &a, DevCtl ctl, cudaStream_t s) {
-  const Spread p = spread_of(a.E, a.dt, (uintptr_t)a.Z % 16 == 0 && (uintptr_t)a.dZ % 16 == 0);
+  const Spread p = spread_of(a.E, a.dt, alignment(a.Z) < alignment(a.dZ) ? alignment(a.Z) : alignment(a.dZ));
   const Grid g = grid_of(a.B, a.N, a.E, a.dt, 4, 0, p);
   cudaError_t e = cudaErrorNotSupported;
   with_spread<T>(p, [&](auto vl, auto np, auto lg) {

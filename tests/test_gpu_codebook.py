@@ -233,6 +233,8 @@ BAL = [  # (B, N, E, M, offset of Z)
     (1, 500, 60, 4, 0), (1, 400, 515, 1, 0), (2, 300, 1024, 2, 0), (1, 200, 1032, 3, 0), (1, 77, 1025, 1, 0), (1, 130, 4096, 6, 0),
     (1, 64, 8192, 64, 0), (1, 33, 8191, 1, 0), (1, 900, 128, 2, 1), (3, 200, 256, 2, 3), (300, 17, 16, 1, 0), (1, 40000, 32, 4, 0),
     (1, 30000, 7, 1, 0), (1, 2500, 288, 2, 0),
+    # rows of whole 4-byte pieces: 16-bit logits in pairs
+    (1, 300, 258, 2, 0), (1, 90, 1026, 1, 0), (1, 40, 8190, 2, 0), (2, 200, 256, 2, 2), (1, 500, 34, 3, 2), (3, 64, 516, 1, 2),
 ]
 
 
