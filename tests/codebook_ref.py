@@ -95,9 +95,13 @@ def balance_grad(r, gloss, coef):
 
 
 def row_range(Z):
-    """R: the largest finite |z| of each row (0 where there is none)."""
-    z = Z.double().abs()
-    return torch.where(torch.isfinite(z), z, torch.zeros((), dtype=torch.float64)).amax(2)
+    """R: the largest finite |z| of each row (0 where there is none) among the
+    logits within 110 of the row's largest; exp of the others is below 2^-126 and
+    counts as 0 on both sides but for the flush that balance_tol adds."""
+    z = Z.double()
+    top = torch.where(torch.isfinite(z), z, torch.full((), -float("inf"), dtype=torch.float64)).amax(2, keepdim=True)
+    near = torch.isfinite(z) & (z >= top - 110)
+    return torch.where(near, z.abs(), torch.zeros((), dtype=torch.float64)).amax(2)
 
 
 def balance_tol(Z, r):
