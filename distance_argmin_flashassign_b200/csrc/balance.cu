@@ -17,12 +17,12 @@
 // not change the result.
 //
 // What bounds it (B200, HBM copy rate 6,466 GB/s): backward HBM, 0.80 of the
-// copy rate from 64 to 8,192 columns (16 x 32,768 x 64 bf16 27.6 us, 1 M x 128
+// copy rate from 64 to 8,192 columns where rows are whole 16-byte pieces (16 x 32,768 x 64 bf16 27.6 us, 1 M x 128
 // 105 us).  Forward issue slots: a bf16 logit takes 8 to 12 instructions with
 // its share of the row's and the tile's, of which the special-function unit
 // serves one (29 us of the 81 us of 1 M x 128 bf16); fp32 rows, half as many
 // logits a byte, reach 0.74 of the copy rate, bf16 rows 0.42 to 0.55.
-// 262,144 x 1,024 fp16: 131 us, 0.64.  Pairs of fp32 operations in one
+// 262,144 x 1,024 fp16: 126 us, 0.66.  Pairs of fp32 operations in one
 // instruction are worth 5 % of it.
 #include <atomic>
 #include <type_traits>
@@ -178,7 +178,7 @@ constexpr int kMaxSmem = 220 * 1024;  // of a block of these kernels, beside som
 constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
 constexpr int kBalLane = 32, kBalSome = 16;  // columns a lane holds at most, and where a warp has lanes to spare
 // Lanes of a team, as a power of two, where the kernel is compiled for them:
-constexpr int kWide = 8;      // the whole block
+constexpr int kWide = 6;      // from here on (64, 128, 256) several warps
 constexpr int kAnyTeam = -1;  // up to a warp, known at run time
 
 // Blocks that fit an SM next to a lane's columns in registers (three with 16
@@ -192,30 +192,43 @@ constexpr int bal_rows(int NE) { return NE <= 16 ? 2 : 1; }
 template <int NE> constexpr int kBalRows = bal_rows(NE);
 
 // Rows go tile by tile to owners: a warp, whose G = 2^logg-lane teams take
-// one row each, or (WIDE) the whole block as one team.  Lane l of a team holds
-// the packs l, l + G, l + 2G, ... of VL columns each.
-template <bool WIDE> struct Owner {
-  int index, count;    // among the owners of the block
+// one row each, or for long rows (WIDE) two, four or eight warps as one team.
+// Lane l of a team holds the packs l, l + G, l + 2G, ... of VL columns each.
+template <int LOGG> struct Owner {
+  static constexpr bool WIDE = LOGG >= kWide;
+  static constexpr int kThreads = WIDE ? 1 << LOGG : 32, kWarps = kThreads / 32, kCount = kBalThreads / kThreads;
+  int index;           // among the owners of the block
   int lane, row0, rows;  // lane in the team, the team's first row of a step, rows of a step
-  int thread, threads;
+  int thread;
   __device__ __forceinline__ explicit Owner(int logg) {
-    index = WIDE ? 0 : threadIdx.x >> 5;
-    count = WIDE ? 1 : kBalWarps;
-    threads = WIDE ? kBalThreads : 32;
-    thread = threadIdx.x % threads;
-    lane = WIDE ? threadIdx.x : threadIdx.x & ((1 << logg) - 1);
+    index = threadIdx.x / kThreads;
+    thread = threadIdx.x % kThreads;
+    lane = WIDE ? thread : threadIdx.x & ((1 << logg) - 1);
     row0 = WIDE ? 0 : (threadIdx.x & 31) >> logg;
     rows = WIDE ? 1 : 32 >> logg;
   }
+  // (the warps are reconverged first and the barriers' per-thread forms are used)
   __device__ __forceinline__ void sync() const {
-    if (WIDE) __syncthreads();
-    else __syncwarp();
+    __syncwarp();
+    if constexpr (kThreads == kBalThreads) __syncthreads();
+    else if constexpr (WIDE) asm volatile("barrier.sync %0, %1;" ::"r"(1 + index), "n"(kThreads) : "memory");
   }
   // sync, and whether any of the owner's threads says so
   __device__ __forceinline__ bool any(bool v) const {
-    if (WIDE) return __syncthreads_or(v) != 0;
     __syncwarp();
-    return __any_sync(0xffffffffu, v) != 0;
+    if constexpr (kThreads == kBalThreads) {
+      return __syncthreads_or(v) != 0;
+    } else if constexpr (WIDE) {
+      int r;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, %3, p;\n\t"
+                   "selp.s32 %0, 1, 0, q;\n\t}"
+                   : "=r"(r)
+                   : "r"((int)v), "r"(1 + index), "n"(kThreads)
+                   : "memory");
+      return r != 0;
+    } else {
+      return __any_sync(0xffffffffu, v) != 0;
+    }
   }
 };
 
@@ -285,7 +298,7 @@ constexpr int kMaxStages = 4;
 struct Bars {
   uint64_t tile[kMaxStages], side[2];
 };
-template <bool WIDE> struct Rows {
+struct Rows {
   const char *Z, *mid, *small;
   uint32_t zrow, midrow;  // bytes of a row (small: 1)
   size_t all;             // rows of the arrays
@@ -338,11 +351,11 @@ template <bool WIDE> struct Rows {
 
 // The calling thread's owner: its rows of problem b and its places, with the
 // barriers set up (visible after the block's next barrier).
-template <bool WIDE>
-__device__ __forceinline__ Rows<WIDE> owned(const Owner<WIDE> &t, const Plan &pl, Bars *bar, char *smem, int b, int B,
+template <int LOGG>
+__device__ __forceinline__ Rows owned(const Owner<LOGG> &t, const Plan &pl, Bars *bar, char *smem, int b, int B,
                                             int N) {
-  Rows<WIDE> v;
-  const long long from = ((long long)blockIdx.x * t.count + t.index) * pl.share;
+  Rows v;
+  const long long from = ((long long)blockIdx.x * t.kCount + t.index) * pl.share;
   v.n = from < N ? (int)min((long long)pl.share, N - from) : 0;
   v.first = (size_t)b * N + from;
   v.all = (size_t)B * N;
@@ -396,23 +409,23 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
                         int B, int N, int E, int M, int logg_, Plan pl, float *__restrict__ lse,
                         float *__restrict__ psum, int *__restrict__ csum, int *__restrict__ tsum, BalanceOut out,
                         DevCtl ctl) {
-  constexpr bool WIDE = LOGG == kWide;
+  constexpr bool WIDE = LOGG >= kWide;
   using L = Lane<T, VL, P>;
   constexpr int NE = L::NE, NP = L::NP, U = kBalRows<NE>;
   extern __shared__ __align__(128) char smem[];
-  __shared__ __align__(8) Bars bars[WIDE ? 1 : kBalWarps];
+  __shared__ __align__(8) Bars bars[Owner<LOGG>::kCount];
   __shared__ float wm[2][U][kBalWarps], wsum[2][U][kBalWarps];
   __shared__ int taken[kBalWarps], abort_flag;
   __shared__ double part[kBalWarps];
   const int logg = LOGG >= 0 ? LOGG : logg_;
-  const Owner<WIDE> t(logg);
+  const Owner<LOGG> t(logg);
   const int b = blockIdx.y, G = 1 << logg;
   // the chosen columns of the block's rows [E], then the owners' places, where
   // the block's column sums [E] lie once the rows are done
   int *hist = reinterpret_cast<int *>(smem);
   char *places = smem + (E * 4 + 15) / 16 * 16;
   float *cols = reinterpret_cast<float *>(places);
-  Rows<WIDE> v = owned<WIDE>(t, pl, &bars[t.index], places, b, B, N);
+  Rows v = owned(t, pl, &bars[t.index], places, b, B, N);
   v.Z = (const char *)Z;
   v.mid = (const char *)ids;
   v.small = (const char *)mask;
@@ -506,22 +519,24 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
               wm[buf][u][threadIdx.x >> 5] = s[u] == 0.f ? neg_inf() : m[u];
               wsum[buf][u][threadIdx.x >> 5] = s[u];
             }
-          __syncthreads();
+          t.sync();
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int r = s0 + u * t.rows + t.row0;
           float factor;  // p_e = z_e w factor
           if (WIDE) {
-            // lane l looks at warp l % 8
-            const float mw = wm[buf][u][threadIdx.x % kBalWarps], sw = wsum[buf][u][threadIdx.x % kBalWarps];
+            // lane l looks at the owner's warp l % kWarps
+            constexpr int KW = Owner<LOGG>::kWarps;
+            const int look = t.index * KW + threadIdx.x % KW;
+            const float mw = wm[buf][u][look], sw = wsum[buf][u][look];
             float top = mw;
 #pragma unroll
-            for (int o = kBalWarps / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = KW / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (top == neg_inf()) top = 0.f;
             sum[u] = sw == 0.f ? 0.f : sw * exp2_fast((mw - top) * kLog2e);
 #pragma unroll
-            for (int o = kBalWarps / 2; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+            for (int o = KW / 2; o > 0; o >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
             // NaN in every warp of a NaN row, 0 in every warp of a row left out
             factor = sum[u] == 0.f ? 0.f : (s[u] == 0.f ? 0.f : exp2_fast((m[u] - top) * kLog2e)) * rcp_fast(sum[u]);
             m[u] = top;
@@ -545,7 +560,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     }
     if (gave_up) break;
     // every thread a row: what is done once for each
-    for (int r = t.thread; r < nrows; r += t.threads) {
+    for (int r = t.thread; r < nrows; r += t.kThreads) {
       const float2 w = stat[r];
       const bool on = w.y != 0.f;  // a masked row has no sum either
       mytok += on;
@@ -562,7 +577,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
   }
   if (gave_up && t.thread == 0) v.drain(kb, kt);
   if (bad) record_status(ctl.status, kStBadLabel);
-  // column sums: over the teams of a warp, then over the warps in order
+  // column sums: over the teams of a warp, then over the owners in order
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kBalThreads) cols[e] = 0.f;
   __syncthreads();
@@ -577,8 +592,8 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     for (int o = G; o < 32; o <<= 1)
 #pragma unroll
       for (int i = 0; i < NE; ++i) sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], o);
-  for (int w = 0; w < (WIDE ? 1 : kBalWarps); ++w) {
-    if (WIDE || ((int)(threadIdx.x >> 5) == w && (threadIdx.x & 31) < G)) {
+  for (int w = 0; w < t.kCount; ++w) {
+    if (t.index == w && (WIDE || (int)(threadIdx.x & 31) < G)) {
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         const int c = (i / VL * G + t.lane) * VL + i % VL;
@@ -685,18 +700,18 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     balance_grad_kernel(const T *Z, const int32_t *__restrict__ counts, const int32_t *__restrict__ tokens,
                         const float *__restrict__ lse, const float *__restrict__ gloss, int B, int N, int E, int M,
                         float coef, int logg_, Plan pl, T *dZ, DevCtl ctl) {
-  constexpr bool WIDE = LOGG == kWide;
+  constexpr bool WIDE = LOGG >= kWide;
   using L = Lane<T, VL, P>;
   constexpr int NE = L::NE, NP = L::NP, U = kBalRows<NE>;
   extern __shared__ __align__(128) char smem[];
-  __shared__ __align__(8) Bars bars[WIDE ? 1 : kBalWarps];
+  __shared__ __align__(8) Bars bars[Owner<LOGG>::kCount];
   __shared__ float wdot[2][U][kBalWarps];
   __shared__ int abort_flag;
   const float inf = __int_as_float(0x7f800000);
   const int logg = LOGG >= 0 ? LOGG : logg_;
-  const Owner<WIDE> t(logg);
+  const Owner<LOGG> t(logg);
   const int b = blockIdx.y, G = 1 << logg;
-  Rows<WIDE> v = owned<WIDE>(t, pl, &bars[t.index], smem, b, B, N);
+  Rows v = owned(t, pl, &bars[t.index], smem, b, B, N);
   v.Z = (const char *)Z;
   v.mid = (const char *)lse;
   v.small = nullptr;
@@ -769,12 +784,12 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
           if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int u = 0; u < U; ++u) wdot[buf][u][threadIdx.x >> 5] = dot[u];
-          __syncthreads();
+          t.sync();
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             dot[u] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kBalWarps; ++w) dot[u] += wdot[buf][u][w];
+            for (int w = 0; w < t.kWarps; ++w) dot[u] += wdot[buf][u][t.index * t.kWarps + w];
           }
           buf ^= 1;
         }
@@ -808,10 +823,11 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 // How a row of E logits is spread: whole 16-byte packs when the rows and the
 // pointers are whole 16-byte pieces, else pairs of 16-bit elements where they
 // are whole 4-byte pieces (262,144 x 258 bf16: 72 us, element by element 89;
-// backward 83 and 123), else single elements; about 16 columns a
-// lane where that needs no more than a warp, up to kBalLane, and from there on
-// the whole block.  Fewer lanes a row exchange less: with 16 columns a lane in
-// place of 8 ...
+// backward 83 and 123), else single elements.  About 16 columns a lane where
+// that needs no more than a warp: fewer lanes a row exchange less (524,288 x 64
+// bf16 of an earlier version: 44 us with 16 columns a lane, 61 with 8).  Then up
+// to kBalLane, and with more columns two, four or eight warps with up to
+// kBalLane a lane (65,536 x 2,048 bf16: 93 us with two, 158 with eight).
 struct Spread {
   int VL, P, logg;
   bool wide;
@@ -826,12 +842,12 @@ static Spread spread_of(int E, DType dt, int aligned) {  // aligned: bytes, of t
   p.VL = unit > (int)dtype_size(dt) ? unit / (int)dtype_size(dt) : 1;
   const int packs = (E + p.VL - 1) / p.VL, most = kBalLane / p.VL, some = kBalSome / p.VL;
   p.wide = packs > 32 * most;
-  const int lanes = p.wide ? kBalThreads : 32;
-  while (!p.wide && p.logg < 5 && (some << p.logg) < packs) ++p.logg;
-  if (p.wide) p.logg = 8;
+  if (p.wide) p.logg = kWide;
+  while ((p.wide || p.logg < 5) && ((p.wide ? most : some) << p.logg) < packs) ++p.logg;
+  const int lanes = p.wide ? 1 << p.logg : 32;
   p.P = 1;
-  // packs a lane: powers of two, and multiples of four from eight on
-  while (p.P * (p.wide ? lanes : 1 << p.logg) < packs) p.P += p.P < 8 ? p.P : 4;
+  // packs a lane: powers of two, and multiples of four (wide: eight) from eight on
+  while (p.P << p.logg < packs) p.P += p.P < 8 ? p.P : p.wide ? 8 : 4;
   p.rows = (lanes >> p.logg) * bal_rows(p.VL * p.P);
   p.resident = bal_blocks(p.VL * p.P);
   p.owners = kBalThreads / lanes;
@@ -931,19 +947,16 @@ template <typename T, typename F> static void with_spread(const Spread &p, F f) 
   if constexpr (H == 4) { FK_P(V, 1, 0) }
   FK_P(V, H / 2, 0)
   FK_P(V, H, 0) FK_P(V, H, 1) FK_P(V, H, 2) FK_P(V, H, 3) FK_P(V, H, 4) FK_P(V, H, 5) FK_P(V, 2 * H, 5)
-  if constexpr (H == 2) { FK_P(V, 1, kWide) }
-  FK_P(V, 2, kWide) FK_P(V, 4, kWide)
-  if constexpr (H == 4) { FK_P(V, 8, kWide) }
+  FK_P(V, 2 * H, 6) FK_P(V, 2 * H, 7) FK_P(V, 2 * H, 8)
   if constexpr (V == 8) {
     FK_P(2, 1, 0) FK_P(2, 2, 0) FK_P(2, 4, 0) FK_P(2, 8, 0) FK_P(2, 8, 1) FK_P(2, 8, 2) FK_P(2, 8, 3) FK_P(2, 8, 4)
     FK_P(2, 8, 5) FK_P(2, 12, 5) FK_P(2, 16, 5)
-    FK_P(2, 4, kWide) FK_P(2, 8, kWide) FK_P(2, 12, kWide) FK_P(2, 16, kWide)
+    FK_P(2, 16, 6) FK_P(2, 16, 7) FK_P(2, 16, 8)
   }
   FK_P(1, 1, 0) FK_P(1, 2, 0) FK_P(1, 4, 0) FK_P(1, 8, 0) FK_P(1, 12, 5) FK_P(1, 16, 5)
   FK_P(1, 12, kAnyTeam) FK_P(1, 16, kAnyTeam)
   FK_P(1, 20, 5) FK_P(1, 24, 5) FK_P(1, 28, 5) FK_P(1, 32, 5)
-  FK_P(1, 8, kWide) FK_P(1, 12, kWide) FK_P(1, 16, kWide) FK_P(1, 20, kWide) FK_P(1, 24, kWide) FK_P(1, 28, kWide)
-  FK_P(1, 32, kWide)
+  FK_P(1, 24, 6) FK_P(1, 32, 6) FK_P(1, 24, 7) FK_P(1, 32, 7) FK_P(1, 24, 8) FK_P(1, 32, 8)
 #undef FK_P
 }
 

@@ -235,6 +235,8 @@ BAL = [  # (B, N, E, M, offset of Z)
     (1, 30000, 7, 1, 0), (1, 2500, 288, 2, 0),
     # rows of whole 4-byte pieces: 16-bit logits in pairs
     (1, 300, 258, 2, 0), (1, 90, 1026, 1, 0), (1, 40, 8190, 2, 0), (2, 200, 256, 2, 2), (1, 500, 34, 3, 2), (3, 64, 516, 1, 2),
+    # rows of several warps, some of which have one row more than others, or none
+    (1, 79, 1025, 1, 0), (1, 3, 2049, 1, 0), (1, 75, 2050, 2, 0), (2, 33, 4097, 1, 0), (1, 1200, 1280, 1, 0), (1, 700, 2560, 2, 0),
 ]
 
 
