@@ -759,17 +759,12 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           x[u].values(z[u]);
-          float top = l[u];
-          if (!kIsHalf<T> && fabsf(top) > 1e38f && top != inf) {  // as in the forward pass
-#pragma unroll
-            for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
-            top = 0.f;
-          }
           float2 dd = both(0.f);
-          const float2 shift = both(-top * kLog2e);
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            z[u][i] = fma2(z[u][i], both(kLog2e), shift);  // past E -inf: a probability of 0
+            // the difference first: a logit that is the row's whole sum has
+            // probability 1 exactly, and so no gradient; past E -inf: 0
+            z[u][i] = mul2(add2(z[u][i], both(-l[u])), both(kLog2e));
             z[u][i].x = exp2_fast(z[u][i].x);
             z[u][i].y = exp2_fast(z[u][i].y);
             dd = fma2(kf[i], z[u][i], dd);
