@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
       // every team a row: probabilities into the column sums, maximum and sum kept
       for (int s0 = 0; s0 < n; s0 += U * t.rows) {
         L x[U];
-        float own[U], m[U], s[U], sum[U];
+        float own[U], off[U], m[U], s[U], sum[U];
         float2 z[U][NP];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -475,13 +475,16 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
           if (own[u] == neg_inf()) own[u] = 0.f;
           x[u].values(z[u]);
           float top = own[u];
-          if (!kIsHalf<T> && fabsf(top) > 1e38f) {  // its product with log2(e) would overflow (the type's lowest values)
+          // a large maximum (a lane of masked columns): the rounding of its product
+          // with log2(e) would be no small exponent any more
+          if (!kIsHalf<T> && fabsf(top) > 65536.f) {
 #pragma unroll
             for (int i = 0; i < NP; ++i) z[u][i] = add2(z[u][i], both(-top));
             top = 0.f;
           }
           float2 ss = both(0.f);
           const float2 shift = both(-top * kLog2e);
+          off[u] = fmaf(top, kLog2e, shift.x);  // the shift's rounding, which the lane's exponentials share
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             z[u][i] = fma2(z[u][i], both(kLog2e), shift);
@@ -500,11 +503,11 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
 #pragma unroll
             for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
         }
-        float w[U];  // exp(own - m): the lane's sum and probabilities on the team's scale
+        float w[U];  // exp(own - m), less that rounding: the lane's sum and probabilities on the team's scale
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (m[u] == neg_inf()) m[u] = 0.f;
-          w[u] = s[u] == 0.f ? 0.f : exp2_fast((own[u] - m[u]) * kLog2e);
+          w[u] = s[u] == 0.f ? 0.f : exp2_fast(fmaf(own[u] - m[u], kLog2e, -off[u]));
           s[u] *= w[u];
         }
 #pragma unroll

@@ -627,3 +627,23 @@ def test_lookup_grad_at_the_digits_edges(K):
     fk.fk_sync()
     g, mag, cnt = ref.lookup_grad(dY[None], ids[None], K, 1.0)
     assert bool(((dT.double() - g[0]).abs() <= ref.lookup_grad_tol(g, mag, cnt, torch.float32)[0]).all())
+
+
+@pytest.mark.parametrize("E", [2, 8, 64, 515, 1024, 2050])
+def test_balance_of_certain_choices(E):
+    """One column switched on, or far ahead of the rest: its probability is 1, its
+    lse its logit and the gradient nothing, to the rounding of 2^x at 0 (4 u), of
+    the sum's logarithm and of lse itself (u each)."""
+    N = 200
+    z = torch.linspace(-90.0, 90.0, N)
+    for rest in (-INF, -1e4, -1e9, -1e30, -3e38):
+        Z = torch.full((N, E), rest)
+        Z[:, E // 2] = z
+        Zd, ids = Z.to(DEV), torch.full((N,), E // 2, dtype=torch.int32, device=DEV)
+        loss, counts, tokens, meanp, lse = fk.fk_balance(Zd, ids)
+        tol = 16 * ref.U + 2 * ref.U * z.abs()
+        assert bool(((lse.cpu() - z).abs() <= tol).all())
+        assert abs(float(meanp[E // 2]) - 1) <= 16 * ref.U and abs(float(loss) - E) <= E * 20 * ref.U
+        dZ = fk.fk_balance_grad(Zd, counts, tokens, lse, 1, gloss=torch.tensor(float(N), device=DEV)).cpu()
+        # E p (1 - p): p is off by the error of lse and 6 u
+        assert bool((dZ.abs().amax(1) <= 1.1 * E * (tol + 6 * ref.U)).all())
