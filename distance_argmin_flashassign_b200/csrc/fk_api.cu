@@ -1043,6 +1043,6 @@ fk_status fk_debug_inject(int what, int64_t at) {
   return FK_OK;
 }
 
-int fk_version(void) { return 101; }
+int fk_version(void) { return 200; }
 
 }  // extern "C"

@@ -500,7 +500,7 @@ FK_API fk_status fk_release_workspace(void);
  * Nothing is injected on the device.  Process-wide. */
 FK_API fk_status fk_debug_inject(int what, int64_t at);
 
-/* Library version, major * 10000 + minor * 100 + patch (101: 0.1.1). */
+/* Library version, major * 10000 + minor * 100 + patch (200: 0.2.0). */
 FK_API int fk_version(void);
 
 #ifdef __cplusplus
