@@ -434,6 +434,8 @@ FK_API fk_status fk_balance(const void *Z, int B, int64_t N, int E, fk_dtype dt,
  *     dZ_ie = g coef E / n * p_ie (f_e - sum_j f_j p_ij)
  *   and 0 in the rows that took no part.  counts, tokens, lse, M and coef as
  *   fk_balance gave or took them.
+ *   lse is an fp32 number: where |lse| > 64, and exp(z - lse) would be off by more
+ *   than 2^-18 of itself, a row's probabilities are divided by their own sum.
  *   gloss  device, B fp32: the loss's own gradient g, or NULL (1)
  *   dZ     device, B x N x E, dtype dt (out); may be Z itself, must not
  *          overlap it otherwise
