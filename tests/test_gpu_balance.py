@@ -6,6 +6,7 @@ import torch
 import distance_argmin_flashassign_b200 as fk
 from tests import balance_bounds as bb
 from tests.parity import TORCH_DT
+from tests.test_gpu_codebook import BAL, _bal_case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -102,3 +103,12 @@ def test_gradient_of_rows_far_from_zero(dt, E):
     ids = torch.zeros(1, N, 1, dtype=torch.int32, device=DEV)
     ids[0, :5] = E - 1
     check(Z, ids, torch.ones(1, N, dtype=torch.bool, device=DEV), 0)
+
+
+@pytest.mark.parametrize("dt", list(SIZE))
+@pytest.mark.parametrize("case", BAL, ids=lambda c: "x".join(map(str, c)))
+def test_cases_of_the_calls_own_tests(case, dt):
+    """The cases of tests/test_gpu_codebook.py, whose bounds there grow with |z|,
+    and so with the type's lowest value in one of their rows."""
+    Z, ids, mask = _bal_case(case, dt)
+    check(Z.to(DEV), ids.to(DEV), mask.to(DEV), case[4])
