@@ -262,6 +262,8 @@ __device__ __noinline__ Span span_at_ends(const char *a, uint32_t n, const char 
   if (hi < lo) hi = lo;
   for (const char *q = a; q < end && q < lo; ++q) dst[q - from] = *q;
   for (const char *q = hi < a ? a : hi; q < end; ++q) dst[q - from] = *q;
+  // the thread's next bulk copy into this place must not overtake these bytes
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   return {lo, (uint32_t)(hi - lo)};
 }
 __device__ __forceinline__ void bulk_copy(const Span &v, const char *a, char *dst, uint32_t bar) {
