@@ -360,7 +360,7 @@ static size_t al256(size_t v) { return (v + 255) / 256 * 256; }
 // clusters, more by a kernel of its own that runs beside the sort.
 constexpr int kFewThreads = 512, kFewWarps = kFewThreads / 32, kFewCtas = 8, kFewItems = 8;
 constexpr int kFewPoints = kFewThreads * kFewItems * kFewCtas;  // 32,768
-constexpr size_t kFewFill = size_t(32) << 20;
+constexpr size_t kFewFill = size_t(64) << 20;
 constexpr int kFewBits = 9, kFewBins = 1 << kFewBits;
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
@@ -550,9 +550,13 @@ static cudaError_t run_sort_few(const int32_t *labels, int B, int N, int K, void
     }
   }
   // beside the sort: one block of 512 threads an SM, with 32 KB to fill at
-  // least.  They write 4 TB/s where a kernel of its own writes 7 (16,384 x
-  // 2,048 bf16 into 131,072 rows, 537 MB: 159 us against 114), but need no
-  // launch: up to kFewFill bytes, what the sort itself takes
+  // least, and no launch of its own, which is worth up to 3 us: a whole gradient
+  // of 256 bf16 columns in a replayed graph takes 16.2 us with 500 labels and a
+  // fill of 64 MiB, 18.7 with a kernel of its own; with 24,000 labels 32.3 and
+  // 34.5 (with 6,000 and 32,768 the kernel is ahead by 1).  But the few fillers'
+  // rate is lower: from 128 MiB on the kernel is ahead with more than some 4,000
+  // labels (36.0 and 44.2 us with 6,000), at 512 MiB from 1,000 on (88 and 93;
+  // 97 and 142 with 16,384).
   const bool apart = fill_bytes > kFewFill;
   long long fillers = apart ? 0 : (long long)((fill_bytes + 32767) / 32768);
   if (fillers > 148) fillers = 148;

@@ -1,6 +1,6 @@
-"""fk_lookup_grad with tables over 32 MiB, whose zero fill is a kernel of its own
-beside the one-launch sort (up to 32,768 labels), and captured calls of more
-labels than that, against sums in 64 bits."""
+"""fk_lookup_grad with large tables, whose zero fill runs beside the one-launch sort
+(up to 32,768 labels) or is a kernel of its own beside it, and captured calls
+of more labels than that, against sums in 64 bits."""
 import pytest
 import torch
 
@@ -48,9 +48,10 @@ def table(K, D, dt, by):
     return v, stands
 
 
-# either side of 2^25 bytes of table, of one launch fewer
+# tables filled by blocks of the sort's own launch, and (over 2^26 bytes) by a kernel beside it
 BIG = [("f32", 32768, 256, 0), ("f32", 32769, 256, 0), ("f32", 70000, 130, 0), ("f32", 70000, 130, 1), ("bf16", 140000, 130, 0),
-       ("bf16", 140000, 130, 1), ("f16", 600001, 33, 1), ("bf16", 131072, 2048, 0)]
+       ("bf16", 140000, 130, 1), ("f16", 600001, 33, 1), ("bf16", 131072, 2048, 0), ("f32", 65536, 256, 0), ("f32", 65537, 256, 0),
+       ("f32", 140000, 130, 1), ("bf16", 270000, 130, 0), ("bf16", 270000, 130, 1), ("f16", 1200001, 33, 3)]
 
 
 @pytest.mark.parametrize("N", [1, 700, 32768])
@@ -69,7 +70,7 @@ def test_tables_filled_beside_the_sort(out, K, D, by, N):
         stands()
 
 
-@pytest.mark.parametrize("N,K,D", [(5000, 70000, 130), (32768, 140000, 64), (40000, 9000, 64), (300000, 70000, 16), (100, 50, 64)])
+@pytest.mark.parametrize("N,K,D", [(5000, 70000, 130), (32768, 300000, 64), (5000, 140001, 130), (40000, 9000, 64), (300000, 70000, 16), (100, 50, 64)])
 def test_captured_on_new_labels(N, K, D):
     """The sort with its fill beside it, and the sort for more labels behind a
     memset, replayed on labels and rows that change, with work before and
