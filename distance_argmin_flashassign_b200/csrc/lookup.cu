@@ -409,8 +409,15 @@ __global__ void __launch_bounds__(256, 3) grad_sum_kernel(const T *__restrict__ 
 // partial rows here, by the warp that looks at chunk q; where it has more than
 // kHotPieces of them, by the block's 32 warps afterwards (warp w adds pieces
 // w, w + 32, ..., then the 32 sums are added in warp order).  blockIdx.y:
-// slice of kJoinCols columns.
-constexpr int kHotPieces = 16, kJoinCols = 512;
+// slice of kJoinCols columns, taken 128 at a time, four a lane (kept
+// as a loop: 1 M x 128 rows of one label take 107 us for the whole gradient, and
+// 147 where the same is written without one).
+// Pieces: with 4 as the border 30,000 x 4,096 rows of 32 labels take 83 us for
+// the whole gradient, with 16 or 64 73; with 64, 16,384 x 2,048 rows of Zipf labels
+// take 94, with 16 79.  Columns: 500 x 1,024 rows of Zipf labels take 16 us with
+// 64 or 128 a block, 24 with 512 (one block adds its slices of a hot label one
+// after another); 1 M x 128 rows of 256 labels take 76 with 64, else 72.
+constexpr int kHotPieces = 16, kJoinCols = 128;
 __global__ void __launch_bounds__(1024) grad_join_kernel(const int32_t *__restrict__ skeys, int rows, int none, int R,
                                                          int D, const float *__restrict__ parts, float scale,
                                                          void *__restrict__ dT, int dt_t, int add) {
