@@ -177,7 +177,8 @@ static fk_status device_state_captured(cudaStream_t s, DevState **out) {
 // Scratch of a codebook call: the caller's (checked against `need`), or the
 // library's for (device, stream).  The library's may be freed when a later
 // call needs more, so a captured call, whose graph would keep the address,
-// has to bring its own.
+// has to bring its own; so has one on cudaStreamPerThread, one handle for a
+// stream of each thread, whose kernels run side by side.
 static fk_status book_scratch(DevState &d, cudaStream_t s, size_t need, void *ws, int64_t ws_bytes, void **out) {
   if (ws) {
     if (ws_bytes < 0 || (size_t)ws_bytes < need)
@@ -187,6 +188,8 @@ static fk_status book_scratch(DevState &d, cudaStream_t s, size_t need, void *ws
     *out = ws;
     return FK_OK;
   }
+  if (s == cudaStreamPerThread)
+    return fail(FK_ERR_UNSUPPORTED, "a call on cudaStreamPerThread needs the caller's workspace");
   bool cap = false;
   const fk_status st = capturing(s, &cap);
   if (st != FK_OK) return st;

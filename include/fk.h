@@ -370,8 +370,9 @@ FK_API fk_status fk_seed_kmeanspp(const void *X, int64_t N, int D, fk_dtype dt, 
  *              least the bytes that the _workspace function returns (a
  *              negative status for invalid sizes), which two calls may share
  *              only if they cannot overlap on the GPU.  With ws = NULL the
- *              library's scratch for (device, stream) is used; a capture
- *              is then refused with FK_ERR_UNSUPPORTED.
+ *              library's scratch for (device, stream) is used; a capture, or
+ *              cudaStreamPerThread (one handle for many streams), is then
+ *              refused with FK_ERR_UNSUPPORTED.
  *   Labels     -1 names nothing (padding, a dropped choice) and is not an
  *              error.  Any other label outside its range is treated as -1 and
  *              reported as FK_ERR_BAD_LABEL by fk_sync().

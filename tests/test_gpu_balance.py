@@ -142,3 +142,20 @@ def test_arrays_that_start_and_end_inside_16_bytes(dt, E, N, M, by):
         assert all(torch.equal(a, b) for a, b in zip(out, first))
     # and the same from lse wherever it lies
     assert torch.equal(fk.fk_balance_grad(Zd, counts, tokens, lse.clone(), M, dZ=placed(Zd, by)), first[5])
+
+
+def test_the_library_has_no_scratch_for_the_per_thread_stream():
+    """cudaStreamPerThread is one handle for a stream of each thread: two threads'
+    kernels would share scratch.  Refused on the host, nothing is written."""
+    X, ids = torch.randn(100, 8, device=DEV), torch.zeros(100, dtype=torch.int32, device=DEV)
+    out = [torch.full((8, 8), 7.0, device=DEV), torch.full((1,), 7.0, device=DEV), torch.full((8,), 7, dtype=torch.int32, device=DEV),
+           torch.full((1,), 7, dtype=torch.int32, device=DEV)]
+    dT, loss, counts, tokens = [t.data_ptr() for t in out]
+    torch.cuda.synchronize()
+    x, i, f32 = X.data_ptr(), ids.data_ptr(), fk.FK_F32
+    for st in (fk.lib.fk_lookup_grad(x, 1, 100, 8, f32, i, 8, 1.0, dT, f32, 0, None, 0, 2),
+               fk.lib.fk_balance(x, 1, 100, 8, f32, i, 1, None, 1.0, loss, counts, tokens, None, None, None, 0, 2)):
+        assert st == fk.FK_ERR_UNSUPPORTED
+        assert "cudaStreamPerThread" in fk.lib.fk_last_error_message().decode()
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in out)
