@@ -14,7 +14,7 @@ The functions carry the C names (see ``include/fk.h``) and take torch tensors:
 * ``fk_lookup(T, ids, scale=1.0)``, ``fk_lookup_grad(dY, ids, K, scale=1.0)``
 * ``fk_balance(Z, ids, mask=None, coef=1.0)``, ``fk_balance_grad(Z, counts, tokens, lse, M, coef=1.0)``
 
-A 3-D ``X`` (B x N x D) selects the batched entry points.  Failures raise
+No call records anything for autograd.  A 3-D ``X`` (B x N x D) selects the batched entry points.  Failures raise
 ``FKError`` carrying the status code and the library's message.
 """
 from __future__ import annotations
@@ -345,6 +345,9 @@ def fk_seed_kmeanspp(X, K, u, centers=None, stream=None):
 # ---------------------------------------------------------- codebook calls --
 # These check every tensor they are given, run on the tensors' device whatever
 # the current one is, and allocate what they return on the stream they run on.
+# They record nothing for autograd (as no call of this module does): results do
+# not require a gradient, whatever the inputs do, and a caller's backward pass
+# makes the gradient calls itself.
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -384,7 +387,8 @@ def _book_workspace(workspace, size, like):
 def fk_lookup(T, ids, scale=1.0, Y=None, dtype=None, stream=None):
     """Rows of a codebook by label: Y = scale * T[ids], in ``dtype`` (T's by
     default); label -1 gives a zero row.  T K x D with ids N, or B x K x D with
-    ids B x N."""
+    ids B x N.  Autograd does not see the call: Y is detached from T, whose
+    gradient ``fk_lookup_grad`` gives."""
     B, K, D, bat = _dims(T)
     N = ids.shape[-1] if ids.dim() else 0
     lead = (B, N) if bat else (N,)
@@ -436,7 +440,8 @@ def fk_balance(Z, ids, mask=None, coef=1.0, loss=None, counts=None, tokens=None,
     with the chosen columns ids (N, or N x M for M choices; B x N (x M)).
     ``mask`` (bool or uint8, N or B x N) leaves padded rows out.  Returns (loss, counts,
     tokens, meanp, lse); the last four are what ``fk_balance_grad`` and a
-    capacity limit need."""
+    capacity limit need.  Autograd does not see the call: the loss is detached
+    from Z, whose gradient ``fk_balance_grad`` gives."""
     B, N, E, bat = _dims(Z)
     lead, top = ((B, N), (B,)) if bat else ((N,), ())
     dt, dev = _dtype(Z), Z.device

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import distance_argmin_flashassign_b200 as fk
+from tests import balance_bounds as bb
 from tests.codebook_ref import U, half_step, tiny
 from tests.parity import TORCH_DT
 
@@ -100,3 +101,30 @@ def test_captured_on_new_labels(N, K, D):
             assert torch.equal(copy, w)
             assert torch.equal(dT, w + w)
             check(copy, y, i)
+
+
+def test_autograd_does_not_see_the_calls():
+    """Results do not require a gradient even where inputs do; the gradient calls
+    give what autograd gives for the plain operations."""
+    N, K, D, E, M = 400, 30, 24, 12, 2
+    g = torch.Generator(device=DEV).manual_seed(9)
+    T = torch.randn(K, D, device=DEV, generator=g, requires_grad=True)
+    Z = torch.randn(N, E, device=DEV, generator=g, requires_grad=True)
+    ids = torch.randint(0, K, (N,), device=DEV, generator=g, dtype=torch.int32)
+    ch = torch.randint(0, E, (N, M), device=DEV, generator=g, dtype=torch.int32)
+    dY = torch.randn(N, D, device=DEV, generator=g)
+    Y = fk.fk_lookup(T, ids, 1.5)
+    loss, counts, tokens, meanp, lse = fk.fk_balance(Z, ch, coef=0.3)
+    assert not any(t.requires_grad for t in (Y, loss, meanp, lse))
+    T64, Z64 = T.detach().double().requires_grad_(), Z.detach().double().requires_grad_()
+    (T64[ids.long()] * 1.5 * dY.double()).sum().backward()
+    f = counts.double() / (M * N)
+    (0.3 * E * (f * torch.softmax(Z64, 1).mean(0)).sum()).backward()
+    dT = fk.fk_lookup_grad(dY, ids, K, 1.5)
+    n = torch.bincount(ids, minlength=K)[:, None]
+    mag = torch.zeros(K, D, device=DEV, dtype=torch.float64).index_add_(0, ids.long(), 1.5 * dY.double().abs())
+    assert bool(((dT.double() - T64.grad).abs() <= 1.01 * (n + 3) * U * mag).all())
+    dZ = fk.fk_balance_grad(Z, counts, tokens, lse, M, coef=0.3)
+    r = bb.balance(Z.detach()[None], ch[None], None, 0.3)
+    t = bb.grad_tol(r, torch.ones(1, device=DEV), 0.3, torch.float32)[0]
+    assert bool(((dZ.double() - Z64.grad).abs() <= t).all())
