@@ -16,14 +16,30 @@
 // order.  Counts are integers, so the shared-memory atomics that make them do
 // not change the result.
 //
-// What bounds it (B200, HBM copy rate 6,466 GB/s): backward HBM, 0.80 of the
-// copy rate from 64 to 8,192 columns where rows are whole 16-byte pieces (16 x 32,768 x 64 bf16 27.6 us, 1 M x 128
-// 105 us).  Forward issue slots: a bf16 logit takes 8 to 12 instructions with
-// its share of the row's and the tile's, of which the special-function unit
-// serves one (29 us of the 81 us of 1 M x 128 bf16); fp32 rows, half as many
-// logits a byte, reach 0.74 of the copy rate, bf16 rows 0.42 to 0.55.
-// 262,144 x 1,024 fp16: 126 us, 0.66.  Pairs of fp32 operations in one
-// instruction are worth 5 % of it.
+// What bounds it (B200; shares of the HBM copy rate of 6,466 GB/s, whole calls
+// back to back).  Forward, latency: with 16 warps an SM (some 120 registers) and
+// chains of dependent operations per row (the maximum and its exchange, two
+// exponentials, the sum's exchange) no unit is full: at 64 columns DRAM 28 %, issue
+// slots 58 %, special-function unit 32 %; at 1,024 55 % each.  A bf16 logit takes
+// 8 to 12 instructions with its share of the row's and the tile's.
+//   16 x 32,768 x 64 bf16  31 us, 0.37     1 M x 128 bf16     80 us, 0.54
+//   262,144 x 1,024 fp16  127 us, 0.65     65,536 x 2,048 bf16  93 us, 0.45
+//   262,144 x 258 bf16     72 us, 0.30     32,768 x 8,192 bf16 227 us, 0.37
+//   262,144 x 256 fp32     65 us, 0.66     100,003 x 515 fp32   61 us, 0.53
+// Backward, HBM where rows are whole 16-byte pieces and there are enough of them,
+// else 2- and 4-byte shared-memory accesses; at 64 columns latency again (DRAM
+// 36 %, issue slots 54 %):
+//   16 x 32,768 x 64 bf16  28 us, 0.76     1 M x 128 bf16    105 us, 0.80
+//   262,144 x 1,024 fp16  205 us, 0.81     65,536 x 2,048 bf16 106 us, 0.78
+//   262,144 x 258 bf16     80 us, 0.53     32,768 x 8,192 bf16 206 us, 0.81
+//   262,144 x 256 fp32     97 us, 0.86     100,003 x 515 fp32   84 us, 0.76
+// Pairs of fp32 operations in one instruction are worth 5 % of the forward pass.
+//
+// Rounding: everything is fp32 (blocks are joined in fp64).  2^x and 1/x are the
+// approximate instructions, 2^-22 and 2^-23 of the result: as much as the
+// rounded products before them cost, and one issue slot in place of several.  A
+// lane adds at most 1,024 rows' probabilities into one fp32 sum, 2^-14 of it
+// at worst; fp64 sums would hold twice the registers at 1/64 of the rate.
 #include <atomic>
 #include <type_traits>
 
@@ -43,9 +59,8 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Two fp32 operations an instruction: the kernels are bound by issue slots
-// before they are by HBM (a logit costs an unpack, half a maximum, half a
-// product and sum each, and one ex2).
+// Two fp32 operations an instruction (a logit costs an unpack, half a maximum,
+// half a product and sum each, and one ex2).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
@@ -183,7 +198,8 @@ constexpr int kAnyTeam = -1;  // up to a warp, known at run time
 
 // Blocks that fit an SM next to a lane's columns in registers (three with 16
 // or more columns a lane spill: 1 M x 128 bf16 100 us against 81 with two, 131,072 x
-// 1,024 112 against 82).
+// 1,024 112 against 82).  With two, 28 of the 233 kernels still spill 12 to 96
+// bytes, all of them single-element ones, with 28 or 32 columns a lane but for one.
 constexpr int bal_blocks(int NE) { return NE <= 8 ? 3 : 2; }
 template <int NE> constexpr int kBalBlocks = bal_blocks(NE);
 // Rows a team works on at a time, so that one row's exchanges between lanes

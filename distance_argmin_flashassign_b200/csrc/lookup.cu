@@ -7,6 +7,9 @@
 // their labels name); its gradient is the sum part of the centroid update and
 // runs on the same sorted order (label_sort.cu): no atomics, every sum in one
 // fixed order.  A label of -1 names no row: a zero row of Y, no part in dT.
+// The sums are fp32, as the update's are: n rows cost n 2^-24 of their magnitudes
+// at worst (2 M rows of Zipf labels: 1.1e-7 of the result measured), two
+// additions an instruction, and fp64 would halve the rows in flight.
 #include <type_traits>
 
 #include "chain.cuh"
@@ -99,7 +102,7 @@ template <typename T, int n> __device__ __forceinline__ void ld_vec(const T *p, 
 // (1 M x 128 fp16 rows of a 1,024-row table: 50 us; with the rows of a step
 // loaded and stored before the next step's are asked for 58 us), with 4 blocks
 // an SM.  Narrow vectors need more of them (50,001 x 1,002 fp32 to bf16, 8-byte
-// loads: 34.5 us with 8, 44 to 47 us with 4) and leave the registers for it.
+// loads: 39 us with 8, 47 with 4) and leave the registers for it.
 template <int EPL> constexpr int kLookDepth = EPL <= 2 ? 8 : 4;
 // Groups of W = 2^logw lanes, one row at a time each; a lane has U vectors of
 // EPL elements in flight: of U rows (W vectors cover a row), or, WIDE, of one
@@ -107,7 +110,11 @@ template <int EPL> constexpr int kLookDepth = EPL <= 2 ? 8 : 4;
 // vectors).  A warp takes 32 consecutive rows at a time: its lanes hold their
 // labels, the next 32 labels are already on their way, and the rows of one
 // step are loaded before those of the step before are scaled and stored, so
-// that neither the labels' nor the rows' round trip is waited for in full.
+// that neither the labels' nor the rows' round trip is waited for in full.  A
+// step has 32 rows at most: where U rows a lane would be more (rows of one or
+// two lanes, with narrow vectors of four), the loads behind them repeat rows of
+// the step and are not stored.  Without them 4 M x 8 bf16 rows take 36.2 us, with
+// them 37.6; but 4 M x 6 (four lanes of pairs) 53.9 and 49.9.
 template <typename TI, typename TO, int EPL, bool WIDE>
 __global__ void __launch_bounds__(256, 4) lookup_kernel(const TI *__restrict__ T, int K, int D,
                                                         const int32_t *__restrict__ ids, int rows, int N, int B,
