@@ -102,24 +102,22 @@ template <typename T, int n> __device__ __forceinline__ void ld_vec(const T *p, 
 // (1 M x 128 fp16 rows of a 1,024-row table: 50 us; with the rows of a step
 // loaded and stored before the next step's are asked for 58 us), with 4 blocks
 // an SM.  Narrow vectors need more of them (50,001 x 1,002 fp32 to bf16, 8-byte
-// loads: 39 us with 8, 47 with 4) and leave the registers for it.
-template <int EPL> constexpr int kLookDepth = EPL <= 2 ? 8 : 4;
+// loads: 39 us with 8, 47 with 4) and leave the registers for it, but a step has
+// 32 rows at most, which rows of one to four lanes fill with four or fewer (2 M x 6
+// bf16, three lanes: 19 us with 4, 27 with 8; 2 M x 10, five lanes: 33 and 31).
+constexpr int look_depth(int epl, int lanes) { return epl <= 2 && lanes > 4 ? 8 : 4; }
 // Groups of W = 2^logw lanes, one row at a time each; a lane has U vectors of
 // EPL elements in flight: of U rows (W vectors cover a row), or, WIDE, of one
 // row (slice blockIdx.y of its columns; one label and one address serve U
 // vectors).  A warp takes 32 consecutive rows at a time: its lanes hold their
 // labels, the next 32 labels are already on their way, and the rows of one
 // step are loaded before those of the step before are scaled and stored, so
-// that neither the labels' nor the rows' round trip is waited for in full.  A
-// step has 32 rows at most: where U rows a lane would be more (rows of one or
-// two lanes, with narrow vectors of four), the loads behind them repeat rows of
-// the step and are not stored.  Without them 4 M x 8 bf16 rows take 36.2 us, with
-// them 37.6; but 4 M x 6 (four lanes of pairs) 53.9 and 49.9.
-template <typename TI, typename TO, int EPL, bool WIDE>
+// that neither the labels' nor the rows' round trip is waited for in full.
+template <typename TI, typename TO, int EPL, int U, bool WIDE>
 __global__ void __launch_bounds__(256, 4) lookup_kernel(const TI *__restrict__ T, int K, int D,
                                                         const int32_t *__restrict__ ids, int rows, int N, int B,
                                                         float scale, TO *__restrict__ Y, int logw, int *status) {
-  constexpr int VB = EPL * (int)sizeof(TI), U = kLookDepth<EPL>;
+  constexpr int VB = EPL * (int)sizeof(TI);
   using V = typename Raw<VB>::type;
   const int lane = threadIdx.x & 31;
   const int W = 1 << logw;
@@ -152,7 +150,8 @@ __global__ void __launch_bounds__(256, 4) lookup_kernel(const TI *__restrict__ T
       for (int u = 0; u < U; ++u) {
         const int k = __shfl_sync(0xffffffffu, k32, (j * take + u * per + sub) & 31);
         v[u] = V();
-        if (k >= 0 && col < D) v[u] = ld_raw<VB>(Tc + (size_t)(unsigned)k * (unsigned)D);
+        // (eight only with eight lanes a row or more: 32 rows)
+        if ((U > 4 || u * per < take) && k >= 0 && col < D) v[u] = ld_raw<VB>(Tc + (size_t)(unsigned)k * (unsigned)D);
       }
     }
   };
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(256, 4) lookup_kernel(const TI *__restrict__ T
 
 template <typename TI, typename TO, int EPL>
 static void launch_lookup_as(const LookupArgs &a, int *status, cudaStream_t s) {
-  constexpr int U = kLookDepth<EPL>;
+  constexpr int U = look_depth(EPL, 32), few = look_depth(EPL, 4);
   const int vecs = a.D / EPL;
   // WIDE from two lanes a row on: a lone lane's 16-byte stores would leave
   // half-written 32-byte sectors behind
@@ -223,7 +222,9 @@ static void launch_lookup_as(const LookupArgs &a, int *status, cudaStream_t s) {
   const long long rows = (long long)a.B * a.N, need = (rows + 255) / 256;
   const long long wave = (148 * 4 + slices - 1) / slices;
   const dim3 grid((unsigned)(need < wave ? need : wave), slices);
-  const auto kernel = wide ? lookup_kernel<TI, TO, EPL, true> : lookup_kernel<TI, TO, EPL, false>;
+  const auto kernel = wide        ? lookup_kernel<TI, TO, EPL, U, true>
+                      : vecs <= 4 ? lookup_kernel<TI, TO, EPL, few, false>
+                                  : lookup_kernel<TI, TO, EPL, U, false>;
   kernel<<<grid, 256, 0, s>>>((const TI *)a.T, a.K, a.D, a.ids, (int)rows, a.N, a.B, a.scale, (TO *)a.Y, logw, status);
 }
 template <typename TI, typename TO> static void launch_lookup_to(const LookupArgs &a, int *status, cudaStream_t s) {
