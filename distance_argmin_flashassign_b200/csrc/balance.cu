@@ -198,7 +198,7 @@ constexpr int kAnyTeam = -1;  // up to a warp, known at run time
 
 // Blocks that fit an SM next to a lane's columns in registers (three with 16
 // or more columns a lane spill: 1 M x 128 bf16 100 us against 81 with two, 131,072 x
-// 1,024 112 against 82).  With two, 28 of the 233 kernels still spill 12 to 96
+// 1,024 112 against 82).  With two, 28 of the 233 kernels still spill 12 to 64
 // bytes, all of them single-element ones, with 28 or 32 columns a lane but for one.
 constexpr int bal_blocks(int NE) { return NE <= 8 ? 3 : 2; }
 template <int NE> constexpr int kBalBlocks = bal_blocks(NE);
@@ -719,9 +719,9 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const float 
 // A row's lse is an fp32 number, so exp(z - lse) is off by up to |lse| 2^-24 of
 // itself: 2^-18 at the border here.  Far from 0 it is not a probability at all
 // (a row filled with -1e9 has the lse -1e9, and exp(z - lse) = 1 in every
-// column): such rows are normalised again.  The question, asked at each step,
-// costs 0 to 2 % (16 x 32,768 x 64 bf16 27.2 us before, 27.7 with it; asked once
-// a batch of rows 29.0).
+// column): such rows are normalised again.  The question, asked at each step
+// (by rows of several warps once a batch of rows), costs 0 to 2 % (16 x 32,768 x 64
+// bf16 27.2 us before, 27.7 with it; asked once a batch there too 29.0).
 __device__ __forceinline__ bool far_lse(float l) {
   return fabsf(l) > 64.f && l != __int_as_float(0x7f800000);  // +inf: a row that takes no part
 }
@@ -770,6 +770,14 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
     const size_t rb = v.first + (size_t)kb * pl.batch;  // the batch's first row
     const int nrows = v.batch_rows(kb);
     const float *ls = reinterpret_cast<const float *>(v.mid_at(kb & 1) + v.skew(v.mid, 4, rb));
+    // WIDE: whether some row of the batch is far, by a vote of the owner's threads,
+    // so that all of them come to the norms' barrier or none does, even where the
+    // wait above has run out and the copy lands while they read
+    bool far_batch = false;
+    if (WIDE) {
+      for (int r = t.thread; r < nrows; r += t.kThreads) far_batch |= far_lse(ls[r]);
+      far_batch = t.any(far_batch);
+    }
     for (int in_batch = 0; in_batch < nrows; in_batch += pl.rows, ++kt) {
       mbar_wait(smem_u32(&v.bar->tile[at]), phase, &abort_flag, ctl);
       const int n = v.tile_rows(kt);
@@ -806,12 +814,15 @@ __global__ void __launch_bounds__(kBalThreads, kBalBlocks<VL * P>)
         for (int o = WIDE ? 16 : G >> 1; o > 0; o >>= 1)
 #pragma unroll
           for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-        bool far = false;
+        bool far = far_batch;
+        if (!WIDE) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) far |= far_lse(l[u]);
-        if (WIDE ? far : __any_sync(0xffffffffu, far) != 0) {
+          for (int u = 0; u < U; ++u) far |= far_lse(l[u]);
+          far = __any_sync(0xffffffffu, far) != 0;
+        }
+        if (far) {
           // such a row's probabilities add up to some other number than 1: they and
-          // the dot product of them are divided by it (WIDE: l is the owner's)
+          // the dot product of them are divided by it
           float norm[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
